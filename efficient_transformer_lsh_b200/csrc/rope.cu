@@ -1,0 +1,168 @@
+// Rotary positions: pairs of a head row's features turned by position * freq.
+//
+// The angle is formed as a phase in turns, by the integer product position *
+// turns modulo 2^64 (turns = freq / 2 pi as a 64-bit fraction): the integer
+// wrap is the reduction modulo one turn, exact at any distance, where a
+// float32 product of position and frequency would lose the phase (0.03 rad
+// at position 2^20). Its top 32 bits, signed, are half turns in [-1, 1).
+//
+// Sine and cosine of a (token, pair) serve every head: a thread keeps those
+// of its pairs in registers and walks the heads.
+#include <algorithm>
+
+#include "internal.h"
+#include "sublayer.cuh"
+#include "sublayer.h"
+
+namespace lsh {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kAhead = 4;   // head rows a thread has in flight
+
+struct RopeArgs {
+  const void* in;
+  void* out;
+  lsh_strides si, so;
+  const uint64_t* turns;
+  const int32_t* pos;
+  int64_t pos0;
+  FastDiv fl, fu;          // L; vectors of a head row (pairs, then copies)
+  int H, L, tokens, tile;  // tile: tokens of a CTA
+  int half, rot, heads;    // rot / 2; heads of a CTA
+  int pair_units, pos_batch;
+  float amp, sign;
+};
+
+// P pairs of one unit: P low and P high features, or 2 P adjacent ones.
+template <class T, int P, bool INTER>
+struct Pairs {
+  Vec<T, INTER ? 2 * P : P> a;
+  Vec<T, INTER ? 1 : P> b;
+  __device__ __forceinline__ void load(const T* p, int second) {
+    a.load(p);
+    if constexpr (!INTER) b.load(p + second);
+  }
+  __device__ __forceinline__ void store(T* p, int second) const {
+    a.store(p);
+    if constexpr (!INTER) b.store(p + second);
+  }
+  __device__ __forceinline__ void turn(const float (&c)[P], const float (&s)[P]) {
+    if constexpr (INTER) {
+      float v[2 * P];
+      a.get(v);
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const float p = v[2 * i], q = v[2 * i + 1];
+        v[2 * i] = p * c[i] - q * s[i];
+        v[2 * i + 1] = q * c[i] + p * s[i];
+      }
+      a.set(v);
+    } else {
+      float v[P], u[P];
+      a.get(v);
+      b.get(u);
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const float p = v[i], q = u[i];
+        v[i] = p * c[i] - q * s[i];
+        u[i] = q * c[i] + p * s[i];
+      }
+      a.set(v);
+      b.set(u);
+    }
+  }
+};
+
+template <class T, int P, bool INTER>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+  const int n = a.tile * (int)a.fu.d;
+  const int h0 = blockIdx.y * a.heads, h1 = min(a.H, h0 + a.heads);
+  for (int j = threadIdx.x; j < n; j += kThreads) {
+    const int tt = (int)a.fu.div((uint32_t)j), u = j - tt * (int)a.fu.d;
+    const int t = blockIdx.x * a.tile + tt;
+    if (t >= a.tokens) return;
+    const int b = (int)a.fl.div((uint32_t)t), l = t - b * a.L;
+    // second: from a pair's first feature to its second (copies: the next P)
+    const bool pair = u < a.pair_units;
+    const int c = pair ? u * (INTER ? 2 * P : P) : a.rot + (u - a.pair_units) * 2 * P;
+    const int second = pair ? a.half : P;
+    float cs[P], sn[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) cs[i] = 1.f, sn[i] = 0.f;
+    if (pair) {
+      const int64_t pos = a.pos0 + (a.pos ? (int64_t)__ldg(a.pos + (int64_t)b * a.pos_batch * a.L + l)
+                                          : (int64_t)l);
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const uint64_t phase = (uint64_t)pos * __ldg(a.turns + u * P + i);
+        // half turns: 24 of the 32 bits survive, an angle error of pi 2^-25
+        sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &sn[i], &cs[i]);
+        cs[i] *= a.amp;
+        sn[i] *= a.amp * a.sign;
+      }
+    }
+    const T* in = (const T*)a.in + (b * a.si.b + l * a.si.l + c);
+    T* out = (T*)a.out + (b * a.so.b + l * a.so.l + c);
+    for (int h = h0; h < h1; h += kAhead) {
+      Pairs<T, P, INTER> r[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (h + k < h1) r[k].load(in + (h + k) * a.si.h, second);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (h + k < h1) {
+          if (pair) r[k].turn(cs, sn);
+          r[k].store(out + (h + k) * a.so.h, second);
+        }
+    }
+  }
+}
+
+template <class T, int P, bool INTER>
+void run(const RopeArgs& a, cudaStream_t s) {
+  const dim3 grid((unsigned)((a.tokens + a.tile - 1) / a.tile),
+                  (unsigned)((a.H + a.heads - 1) / a.heads));
+  rope_kernel<T, P, INTER><<<grid, kThreads, 0, s>>>(a);
+}
+template <class T, int P>
+void run_order(const RopeArgs& a, bool inter, cudaStream_t s) {
+  inter ? run<T, P, true>(a, s) : run<T, P, false>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const lsh_rope_problem& q, const lsh_strides& sin, const lsh_strides& sout,
+                        const void* in, const uint64_t* turns, const int32_t* pos, int64_t pos0,
+                        void* out, bool inverse, int vp, cudaStream_t s) {
+  RopeArgs a{};
+  a.in = in, a.out = out, a.si = sin, a.so = sout;
+  a.turns = turns, a.pos = pos, a.pos0 = pos0;
+  a.H = q.H, a.L = q.L, a.tokens = q.B * q.L;
+  a.half = q.rot / 2, a.rot = q.rot;
+  a.pair_units = a.half / vp;
+  const int units = a.pair_units + (q.d - q.rot) / (2 * vp);
+  a.fl = FastDiv((uint32_t)q.L), a.fu = FastDiv((uint32_t)units);
+  a.pos_batch = q.pos_batch;
+  a.amp = q.amp, a.sign = inverse ? -1.f : 1.f;
+  a.tile = std::max(1, kThreads / units);
+  // enough CTAs for the GPU before a thread walks more heads
+  const int64_t ctas = ((int64_t)a.tokens + a.tile - 1) / a.tile;
+  const int64_t split = std::min<int64_t>((q.H + kAhead - 1) / kAhead,
+                                          std::max<int64_t>(1, 148 * 8 / ctas));
+  a.heads = (int)((q.H + split - 1) / split);
+  if (q.dtype == LSH_BF16) {
+    if (vp == 8) run<__nv_bfloat16, 8, false>(a, s);
+    else if (vp == 4) run_order<__nv_bfloat16, 4>(a, q.interleaved, s);
+    else if (vp == 2) run_order<__nv_bfloat16, 2>(a, q.interleaved, s);
+    else run_order<__nv_bfloat16, 1>(a, q.interleaved, s);
+  } else {
+    if (vp == 4) run<float, 4, false>(a, s);
+    else if (vp == 2) run_order<float, 2>(a, q.interleaved, s);
+    else run_order<float, 1>(a, q.interleaved, s);
+  }
+  note_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace lsh

@@ -1,0 +1,166 @@
+// Device helpers of the sublayer operators: vectors of V elements, division
+// by a launch constant, and the dropout's random lanes.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace lsh {
+
+// V consecutive elements of type T as 32-bit words (one half word for V = 1
+// bf16), loaded and stored in accesses of at most 16 bytes.
+template <class T, int V>
+struct Vec {
+  static constexpr int kBytes = V * (int)sizeof(T);
+  static constexpr int kWords = kBytes < 4 ? 1 : kBytes / 4;
+  uint32_t w[kWords];
+
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (kBytes == 2) {
+      w[0] = *reinterpret_cast<const unsigned short*>(p);
+    } else if constexpr (kBytes == 4) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (kBytes == 8) {
+      const uint2 u = *reinterpret_cast<const uint2*>(p);
+      w[0] = u.x;
+      w[1] = u.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kBytes / 16; ++i) {
+        const uint4 u = reinterpret_cast<const uint4*>(p)[i];
+        w[4 * i] = u.x;
+        w[4 * i + 1] = u.y;
+        w[4 * i + 2] = u.z;
+        w[4 * i + 3] = u.w;
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (kBytes == 2) {
+      *reinterpret_cast<unsigned short*>(p) = (unsigned short)w[0];
+    } else if constexpr (kBytes == 4) {
+      *reinterpret_cast<uint32_t*>(p) = w[0];
+    } else if constexpr (kBytes == 8) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kBytes / 16; ++i)
+        reinterpret_cast<uint4*>(p)[i] =
+            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[V]) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = __uint_as_float(w[i]);
+    } else if constexpr (V == 1) {
+      v[0] = __uint_as_float(w[0] << 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    }
+  }
+  // bf16: round to nearest even.
+  __device__ __forceinline__ void set(const float (&v)[V]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) w[i] = __float_as_uint(v[i]);
+    } else if constexpr (V == 1) {
+      w[0] = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<uint32_t*>(&h);
+      }
+    }
+  }
+};
+
+// V consecutive float32 parameters.
+template <int V>
+__device__ __forceinline__ void load_params(const float* p, float (&v)[V]) {
+  if constexpr (V % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) {
+      const float4 u = __ldg(reinterpret_cast<const float4*>(p) + i);
+      v[4 * i] = u.x;
+      v[4 * i + 1] = u.y;
+      v[4 * i + 2] = u.z;
+      v[4 * i + 3] = u.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = __ldg(p + i);
+  }
+}
+
+// n / d and n mod d for 0 <= n < 2^31 by one multiplication: with s =
+// ceil(log2 d) and m = ceil(2^(32+s) / d) - 2^32, (umulhi(n, m) + n) >> s is
+// the quotient for every 32-bit n, and the sum stays below 2^32 for n < 2^31.
+struct FastDiv {
+  uint32_t d, m, s;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t div) : d(div), s(0) {
+    while ((1ull << s) < d) ++s;
+    m = (uint32_t)((((1ull << s) - d) << 32) / d + 1);
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const {
+    return (__umulhi(n, m) + n) >> s;
+  }
+};
+
+// Ten rounds of Philox4x32 (Salmon et al., SC 2011): two 32 x 32 -> 64-bit
+// products a round, keys stepped by two odd constants.
+struct Philox {
+  uint32_t k0, k1, c2, c3;
+  __device__ __forceinline__ Philox(uint64_t seed, uint64_t offset)
+      : k0((uint32_t)seed), k1((uint32_t)(seed >> 32)), c2((uint32_t)offset),
+        c3((uint32_t)(offset >> 32)) {}
+  __device__ __forceinline__ uint4 operator()(uint64_t n) const {
+    uint32_t x0 = (uint32_t)n, x1 = (uint32_t)(n >> 32), x2 = c2, x3 = c3, a = k0, b = k1;
+#pragma unroll
+    for (int r = 0; r < 10; ++r) {
+      const uint64_t p = (uint64_t)x0 * 0xD2511F53u, q = (uint64_t)x2 * 0xCD9E8D57u;
+      x0 = (uint32_t)(q >> 32) ^ x1 ^ a;
+      x1 = (uint32_t)q;
+      x2 = (uint32_t)(p >> 32) ^ x3 ^ b;
+      x3 = (uint32_t)p;
+      a += 0x9E3779B9u;
+      b += 0xBB67AE85u;
+    }
+    return make_uint4(x0, x1, x2, x3);
+  }
+};
+
+// v[i] = kept ? v[i] * scale : 0 for the V features starting at feature c of
+// a row whose groups of 8 start at counter n0 (V = 8: c is a multiple of 8).
+template <int V>
+__device__ __forceinline__ void drop(float (&v)[V], const Philox& rng, uint64_t n0, int c,
+                                     uint32_t t, float scale) {
+  static_assert(V == 8 || V == 1, "a whole group or one element");
+  const uint4 r = rng(n0 + (uint32_t)c / 8);
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  if constexpr (V == 8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t lane = (i & 1) ? w[i / 2] >> 16 : w[i / 2] & 0xffffu;
+      v[i] = lane >= t ? v[i] * scale : 0.f;
+    }
+  } else {
+    const int i = c & 7;
+    const uint32_t u = (i & 4) ? ((i & 2) ? w[3] : w[2]) : ((i & 2) ? w[1] : w[0]);
+    const uint32_t lane = (i & 1) ? u >> 16 : u & 0xffffu;
+    v[0] = lane >= t ? v[0] * scale : 0.f;
+  }
+}
+
+}  // namespace lsh

@@ -240,6 +240,168 @@ lsh_status lsh_rev_bwd(const lsh_problem* p, const lsh_ff_problem* f, const void
                        float* dW2, float* db2, void* ws, size_t ws_bytes, lsh_stream_t stream);
 
 /*
+ * Around a sublayer: norms before and after it, its gate and residual scale,
+ * dropout and rotary positions. Activations are [B, H, L, d] in `dtype`
+ * (float32 or bf16); token (b, l) has D = H d features, its H head rows side
+ * by side, and norms run over a token's D features. All arithmetic is
+ * float32; a bf16 result is rounded once (to nearest even). Parameters and
+ * their gradients are float32.
+ *
+ * Layout: element (b, h, l, c) of an activation is at b*s.b + h*s.h + l*s.l
+ * + c elements from its pointer (the features of a head row are adjacent).
+ * A problem names the strides of each group of activations; all three zero
+ * means the contiguous [B, H, L, d]. Strides of dimensions longer than 1 are
+ * positive and describe distinct elements (no expanded dimensions).
+ * Activations need the alignment of their element type; when pointers and
+ * strides are multiples of 16 bytes and d of 8, the wide-access kernels run.
+ *
+ * An output activation may be the same array (pointer and strides) as an
+ * activation input of the same call; any other overlap, and two outputs that
+ * overlap, give undefined values. At most 2^30 rows (B H L). B*L == 0 launches no activation kernel; parameter gradients are
+ * then written as zeros. Nothing here uses the device status word.
+ */
+typedef struct {
+  int64_t b, h, l;
+} lsh_strides;
+
+typedef enum { LSH_NORM_NONE = 0, LSH_NORM_LAYER = 1, LSH_NORM_RMS = 2 } lsh_norm_kind;
+typedef enum { LSH_GATE_NONE = 0, LSH_GATE_VECTOR = 1, LSH_GATE_SIGMOID = 2 } lsh_gate_kind;
+
+/*
+ * lsh_norm_fwd: h = xhat w + b, xhat = (x - m) r over a token's D features,
+ *   r = 1 / sqrt(mean (x - m)^2 + eps), m = mean x (LSH_NORM_LAYER) or 0
+ *   (LSH_NORM_RMS). w, b: [D], NULL = ones, zeros. h may be x.
+ * lsh_norm_bwd: the gradients of sum(h * dh), the statistics recomputed from
+ *   x: dx = dres + dL/dx (dres may be NULL), dw = sum dh xhat, db = sum dh
+ *   over all tokens (each may be NULL: not computed), overwritten. dx may be
+ *   x, dh or dres. The sums over tokens run in a fixed order: results are the
+ *   same from run to run.
+ *   D at most 8192 (else LSH_ERR_UNSUPPORTED).
+ */
+typedef struct {
+  int32_t B, H, L, d;
+  int32_t dtype;        /* lsh_dtype of x, h and their gradients               */
+  int32_t kind;         /* LSH_NORM_LAYER or LSH_NORM_RMS                      */
+  float eps;            /* > 0                                                 */
+  lsh_strides x;        /* x, dres, dx                                         */
+  lsh_strides h;        /* h, dh                                               */
+} lsh_norm_problem;
+
+lsh_status lsh_norm_fwd(const lsh_norm_problem* n, const void* x, const float* w, const float* b,
+                        void* h, lsh_stream_t stream);
+size_t lsh_norm_bwd_workspace_size(const lsh_norm_problem* n);
+lsh_status lsh_norm_bwd(const lsh_norm_problem* n, const void* x, const float* w, const void* dh,
+                        const void* dres, void* dx, float* dw, float* db, void* ws,
+                        size_t ws_bytes, lsh_stream_t stream);
+
+/*
+ * lsh_dropout_fwd: y = x * 65536 / (65536 - t) where kept, else 0, with
+ *   t = round(65536 p), so p is taken to the nearest 2^-16 and the scale is
+ *   that of the p taken (t = 65536 keeps nothing). The mask is never stored:
+ *   element c of the row r = (slice0 + b H + h) L + l is kept when lane c
+ *   mod 8 (16 bits, low half of each word first) of
+ *     Philox4x32-10(key = seed, counter = (r ceil(d/8) + c/8, offset'))
+ *   (64-bit key and counter halves, low word first; Salmon, Moraes, Dror and
+ *   Shaw, "Parallel random numbers: as easy as 1, 2, 3", SC 2011) is >= t.
+ *   It depends on (seed, offset', position) alone, not on layout, alignment
+ *   or launch, so a reversible layer's recomputation sees the forward's mask,
+ *   and the same call on dy is the backward pass. slice0 is the global index
+ *   of the problem's first (b, h) slice when ranks hold shards of one problem.
+ *   offset' = offset + *counter, or offset when counter is NULL. `counter`
+ *   is a device pointer read when the kernel runs: a captured graph replayed
+ *   after the counter changed drops other elements.
+ *   Dropped elements are 0 whatever x holds.
+ */
+typedef struct {
+  int32_t B, H, L, d;
+  int32_t dtype;
+  float p;              /* 0 <= p <= 1                                         */
+  int64_t slice0;       /* >= 0                                                */
+  lsh_strides x, y;
+} lsh_dropout_problem;
+
+lsh_status lsh_dropout_fwd(const lsh_dropout_problem* q, const void* x, uint64_t seed,
+                           uint64_t offset, const uint64_t* counter, void* y,
+                           lsh_stream_t stream);
+
+/*
+ * lsh_residual_fwd: what joins a sublayer's output f to its residual input x:
+ *     y = beta x + alpha drop(gate * u),  u = post(f) = fhat w_post + b_post
+ *     h = norm(y) = yhat w + b            (the next sublayer's input)
+ *   post and norm are norms as above, or LSH_NORM_NONE (u = f; h not
+ *   written). gate: none; LSH_GATE_VECTOR, a float32 vector [D], or [B, D]
+ *   with gate_batch; LSH_GATE_SIGMOID, gate = 1 / (1 + exp(-z)) of an
+ *   activation z like f. drop as in lsh_dropout_fwd (p = 0: none; element
+ *   indices of [B, H, L, d]). h is the norm of y as stored, bit for bit what
+ *   lsh_norm_fwd(y) gives: a reversible layer recomputes h from the stored y.
+ *   w, b, w_post, b_post may be NULL (ones, zeros).
+ *   With (alpha, beta) replaced by (-alpha/beta, 1/beta), x := y and no norm
+ *   it is the inverse: it rebuilds x from y and f.
+ * lsh_residual_bwd: gradients of sum(y * dy) + sum(h * dh) (dy may be NULL:
+ *   zeros), from y and f: T = dy + norm_bwd(dh); dx = beta T (may be NULL);
+ *   df, dgate, dw_post, db_post, dw, db as the formulas give (the vectors may
+ *   each be NULL: not computed). dgate is like the gate: float32 [D] or
+ *   [B, D], or an activation like z. y and dh are read only with a norm,
+ *   b_post only for a vector gate's or sigmoid's gradient. Sums over tokens
+ *   run in a fixed order. D at most 8192.
+ */
+typedef struct {
+  int32_t B, H, L, d;
+  int32_t dtype;
+  int32_t post, norm;   /* lsh_norm_kind                                       */
+  int32_t gate;         /* lsh_gate_kind                                       */
+  int32_t gate_batch;   /* LSH_GATE_VECTOR: 0: [D]; 1: [B, D]                  */
+  float eps_post, eps;  /* > 0                                                 */
+  float alpha, beta;    /* finite                                              */
+  float p;              /* 0 <= p <= 1                                         */
+  int64_t slice0;       /* >= 0                                                */
+  lsh_strides x;        /* x, y, h, dy, dh, dx                                 */
+  lsh_strides f;        /* f, z, df, dz                                        */
+} lsh_residual_problem;
+
+lsh_status lsh_residual_fwd(const lsh_residual_problem* q, const void* x, const void* f,
+                            const void* gate, const float* w_post, const float* b_post,
+                            const float* w, const float* b, uint64_t seed, uint64_t offset,
+                            const uint64_t* counter, void* y, void* h, lsh_stream_t stream);
+size_t lsh_residual_bwd_workspace_size(const lsh_residual_problem* q);
+lsh_status lsh_residual_bwd(const lsh_residual_problem* q, const void* dy, const void* dh,
+                            const void* y, const void* f, const void* gate, const float* w_post,
+                            const float* b_post, const float* w, uint64_t seed, uint64_t offset,
+                            const uint64_t* counter, void* dx, void* df, void* dgate,
+                            float* dw_post, float* db_post, float* dw, float* db, void* ws,
+                            size_t ws_bytes, lsh_stream_t stream);
+
+/*
+ * lsh_rope_fwd: rotary positions. The first `rot` features of every head row
+ *   turn in pairs, (2i, 2i+1) when interleaved, else (i, i + rot/2), by the
+ *   angle position * freq_i: (p, q) -> amp (p cos - q sin, q cos + p sin);
+ *   the other d - rot features are copied. turns[i] (device, uint64[rot/2])
+ *   is freq_i / (2 pi) modulo 1 as a 64-bit fraction, so that position *
+ *   turns[i] modulo 2^64 is the exact phase at any distance: an angle formed
+ *   in float32 is off by 0.03 at position 2^20. Position scalings for long
+ *   contexts are choices of turns and amp.
+ *   Position of token (b, l): pos0 + (pos ? pos[b pos_batch L + l] : l), any
+ *   sign.
+ * lsh_rope_bwd: dx = amp * the opposite turn of dy (the transposed map); the
+ *   strides y belong to dy and x to dx.
+ *   rot and d even, 2 <= rot <= d <= 512.
+ */
+typedef struct {
+  int32_t B, H, L, d;
+  int32_t dtype;
+  int32_t rot;
+  int32_t interleaved;  /* 0 or 1                                              */
+  int32_t pos_batch;    /* pos: 0: [L], shared by the batch; 1: [B, L]         */
+  float amp;            /* finite                                              */
+  lsh_strides x, y;
+} lsh_rope_problem;
+
+lsh_status lsh_rope_fwd(const lsh_rope_problem* q, const void* x, const uint64_t* turns,
+                        const int32_t* pos, int64_t pos0, void* y, lsh_stream_t stream);
+lsh_status lsh_rope_bwd(const lsh_rope_problem* q, const void* dy, const uint64_t* turns,
+                        const int32_t* pos, int64_t pos0, void* dx, lsh_stream_t stream);
+
+/*
  * lsh_sort_noalloc — lsh_sort without a caller workspace. The reference pages
  *   have no counterpart: this entry point exists for callers that cannot
  *   obtain device memory for a workspace, such as a host framework that owns
