@@ -1,0 +1,372 @@
+// Backward of the norms and the residual add; see norm_residual.cuh.
+//
+// Parameter gradients are sums over tokens. Every thread keeps its features'
+// sums in registers over all the tokens it visits; a CTA writes one row of
+// partial sums, and a second kernel adds the rows in order: no atomics, the
+// same result every time. Four sums suffice, per group of tokens that shares
+// a gate vector: A = sum dh yhat, B = sum dh, S1 = sum q fhat, S0 = sum q
+// (q before the gate; du for a sigmoid gate):
+//   dw = A, db = B, dw_post = gate S1, db_post = gate S0,
+//   dgate = w_post S1 + b_post S0.
+//
+// A row needs at most three sums over its features: both means; then squared
+// deviations of y and f, a and a (y - mean) together (a does not depend on the
+// statistics, so r is factored out: mean(a yhat) = r mean(a (y - mean))); then
+// the second norm's a and a (f - mean).
+#include "norm_residual.cuh"
+
+namespace lsh {
+namespace {
+
+constexpr int kBwdPer = 16;   // features a thread
+
+// A CTA's row of partial sums: the teams' sums are added in order.
+template <class At>
+__device__ __forceinline__ void write_part(const At& at, const f2 (&s)[At::P], float* out,
+                                           float* buf) {
+  constexpr int V = At::P * 2 / At::NV;
+  const SubArgs& a = at.a;
+  __syncthreads();
+  float* row = buf + at.team_id * a.D;
+#pragma unroll
+  for (int i = 0; i < At::P; ++i) {
+    const float2 u = up(s[i]);
+    const int k0 = 2 * i / V, k1 = (2 * i + 1) / V;
+    if (at.on(k0)) row[at.feat(k0) + 2 * i % V] = u.x;
+    if (at.on(k1)) row[at.feat(k1) + (2 * i + 1) % V] = u.y;
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
+    float t = 0.f;
+    for (int w = 0; w < a.teams; ++w) t += buf[w * a.D + c];
+    out[c] = t;
+  }
+}
+
+// Parameters, in order: W, P1 = gate w_post (a sigmoid gate is not in it), P0
+// = b_post (sigmoid gates only).
+template <class T, int V, int PER, int TEAM, bool BRANCH, bool NORM>
+__global__ void __launch_bounds__(TEAM == 0 ? 32 * kMaxWarps : kTeamThreads, TEAM == 0 ? 1 : 2)
+sub_bwd_kernel(const __grid_constant__ SubArgs a) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  using At = Place<T, V, PER, TEAM, (NORM ? 1 : 0) + (BRANCH ? 2 : 0)>;
+  constexpr int P = At::P;
+  constexpr int kP1 = NORM ? 1 : 0, kP0 = kP1 + 1;
+  At at(a, smem);
+  const bool post = BRANCH && a.post != LSH_NORM_NONE;
+  const bool sig = BRANCH && a.gate == LSH_GATE_SIGMOID;
+  const float* gv = a.gv ? a.gv + (int64_t)at.group * (a.gate_batch ? a.D : 0) : nullptr;
+  const bool has1 = BRANCH && (a.wp || gv), has0 = sig && a.bp;
+  if (NORM && a.w) at.stage_param(0, a.w, nullptr);
+  if (has1) at.stage_param(kP1, a.wp, gv);
+  if (has0) at.stage_param(kP0, a.bp, nullptr);
+  // the ring's tensors: y dh, dy, f, z
+  const int i_dy = NORM ? 2 : 0, i_f = i_dy + (a.dy ? 1 : 0), i_z = i_f + 1;
+  const int tensors = i_f + BRANCH + sig;
+  at.clear(at.ring, a.stages * tensors);
+  __syncthreads();
+  const Philox rng(a.seed, a.offset + (a.counter ? __ldg(a.counter) : 0));
+  const int step = at.step(), rounds = at.rounds();
+  const uint32_t one = at.tensor();
+  const uint32_t stage_bytes = tensors * one;
+  f2 sa[P], sb[P], s1[P], s0[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) sa[i] = sb[i] = s1[i] = s0[i] = 0ull;
+
+  int t_in = at.first(), n_in = 0;
+  uint32_t s_in = at.ring;
+  auto copy = [&]() {
+    if constexpr (At::kRing) {
+      if (n_in < rounds) {
+        if (t_in < a.tokens) {
+          int b, l;
+          at.token(t_in, b, l);
+          const int64_t rx = At::row(a.sx, b, l);
+          if constexpr (NORM) {
+            at.issue(a.x, at.ox, rx, s_in);
+            at.issue(a.dh, BRANCH ? at.ox : at.oh, BRANCH ? rx : At::row(a.sh, b, l), s_in + one);
+          }
+          if (a.dy) at.issue(a.dy, at.ox, rx, s_in + i_dy * one);
+          if constexpr (BRANCH) {
+            const int64_t rf = At::row(a.sf, b, l);
+            at.issue(a.f, at.of, rf, s_in + i_f * one);
+            if (sig) at.issue(a.z, at.of, rf, s_in + i_z * one);
+          }
+        } else {
+          // nothing may be added for a token that is not there
+          at.clear(s_in, tensors);
+        }
+        t_in += step;
+        ++n_in;
+        s_in += stage_bytes;
+        if (s_in == at.ring + a.stages * stage_bytes) s_in = at.ring;
+      }
+      cp_commit();
+    }
+  };
+  for (int i = 1; i < a.stages; ++i) copy();
+  uint32_t st = at.ring;
+  int t = at.first();
+  for (int n = 0; n < rounds; ++n, t += step) {
+    copy();
+    if constexpr (At::kRing) cp_wait_for(a.stages - 1);
+    const bool live = At::kMulti || t < a.tokens;
+    int b, l;
+    at.token(t, b, l);
+    f2 q[P];     // T, then q, then du
+    f2 hat[P];   // y - mean, then f - mean, then fhat
+    float r_f = 0.f, mean_f = 0.f;
+    if constexpr (NORM) {
+      at.get(a.x, a.sx, b, l, live, st, hat);
+      const bool lf = post && a.post == LSH_NORM_LAYER, ly = a.norm == LSH_NORM_LAYER;
+      if (lf || ly) {
+        float s[2] = {0.f, 0.f};
+        if (ly) s[0] = sum_all(hat);
+        if (lf) {
+          f2 f[P];
+          at.get(a.f, a.sf, b, l, live, st + i_f * one, f);
+          s[1] = sum_all(f);
+        }
+        at.team_sum(s);
+        if (ly) at.center(hat, s[0] * a.inv_d);
+        mean_f = s[1] * a.inv_d;
+      }
+      float s[4];
+      s[3] = 0.f;
+      if (post) {
+        f2 f[P];
+        at.get(a.f, a.sf, b, l, live, st + i_f * one, f);
+        if (lf) at.center(f, mean_f);
+        s[3] = dot_all(f, f);
+      }
+      s[0] = dot_all(hat, hat);
+      at.get(a.dh, a.sh, b, l, live, st + one, q);
+#pragma unroll
+      for (int i = 0; i < P; ++i) sb[i] = add2(sb[i], q[i]);
+      if (a.w) at.scale_by(0, q);
+      s[1] = sum_all(q);
+      s[2] = dot_all(q, hat);
+      at.team_sum(s);
+      const float r = inv_std(s[0], a.inv_d, a.eps);
+      if (post) r_f = inv_std(s[3], a.inv_d, a.eps_post);
+      const float m0 = ly ? s[1] * a.inv_d : 0.f, m1 = r * r * s[2] * a.inv_d;
+      const f2 r2 = pk(r, r), nm0 = pk(-m0, -m0), nm1 = pk(-m1, -m1);
+      {
+        f2 dh[P];
+        at.get(a.dh, a.sh, b, l, live, st + one, dh);
+#pragma unroll
+        for (int i = 0; i < P; ++i) sa[i] = fma2(dh[i], mul2(hat[i], r2), sa[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < P; ++i) q[i] = mul2(r2, fma2(hat[i], nm1, add2(q[i], nm0)));
+      if (a.dy) {
+        f2 dy[P];
+        at.get(a.dy, a.sx, b, l, live, st + i_dy * one, dy);
+#pragma unroll
+        for (int i = 0; i < P; ++i) q[i] = add2(q[i], dy[i]);
+      }
+    } else {
+      at.get(a.dy, a.sx, b, l, live, st + i_dy * one, q);
+    }
+    if (a.dx) {
+      f2 o[P];
+#pragma unroll
+      for (int i = 0; i < P; ++i) o[i] = q[i];
+      if (BRANCH && a.beta != 1.f) scale_all(o, a.beta);
+      at.template put<false>(a.dx, a.sx, at.ox, b, l, live, o);
+    }
+    if constexpr (BRANCH) {
+      at.get(a.f, a.sf, b, l, live, st + i_f * one, hat);
+      if (post) {
+        if constexpr (NORM) {
+          if (a.post == LSH_NORM_LAYER) at.center(hat, mean_f);
+        } else {
+          float s[1];
+          if (a.post == LSH_NORM_LAYER) {
+            s[0] = sum_all(hat);
+            at.team_sum(s);
+            at.center(hat, s[0] * a.inv_d);
+          }
+          s[0] = dot_all(hat, hat);
+          at.team_sum(s);
+          r_f = inv_std(s[0], a.inv_d, a.eps_post);
+        }
+        scale_all(hat, r_f);
+      }
+      if (a.drop_t) at.drop_all(rng, b, l, a.alpha * a.drop_scale, q);
+      else scale_all(q, a.alpha);
+      if (sig) {
+        f2 u[P], z[P];
+#pragma unroll
+        for (int i = 0; i < P; ++i) u[i] = hat[i];
+        if (post && a.wp) at.scale_by(kP1, u);
+        if (has0) at.shift_by(kP0, u);
+        at.get(a.z, a.sf, b, l, live, st + i_z * one, z);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const float2 w = up(z[i]);
+          float d0, d1;
+          const float g0 = sigmoid(w.x, d0), g1 = sigmoid(w.y, d1);
+          u[i] = mul2(u[i], mul2(q[i], pk(d0, d1)));
+          q[i] = mul2(q[i], pk(g0, g1));
+        }
+        if (a.dz) at.template put<false>(a.dz, a.sf, at.of, b, l, live, u);
+      }
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        s1[i] = fma2(q[i], hat[i], s1[i]);
+        s0[i] = add2(s0[i], q[i]);
+      }
+      if (has1) at.scale_by(kP1, q);
+      if (post) {
+        float s[2] = {sum_all(q), dot_all(q, hat)};
+        at.team_sum(s);
+        const float m0 = a.post == LSH_NORM_LAYER ? s[0] * a.inv_d : 0.f, m1 = s[1] * a.inv_d;
+        const f2 r2 = pk(r_f, r_f), nm0 = pk(-m0, -m0), nm1 = pk(-m1, -m1);
+#pragma unroll
+        for (int i = 0; i < P; ++i) q[i] = mul2(r2, fma2(hat[i], nm1, add2(q[i], nm0)));
+      }
+      at.template put<false>(a.df, a.sf, at.of, b, l, live, q);
+    }
+    st += stage_bytes;
+    if (st == at.ring + a.stages * stage_bytes) st = at.ring;
+  }
+  if constexpr (At::kRing) cp_wait<0>();
+  if (a.part) {
+    constexpr int kVecs = (NORM ? 2 : 0) + (BRANCH ? 2 : 0);
+    float* out = a.part + (int64_t)blockIdx.x * kVecs * a.D;
+    float* buf = reinterpret_cast<float*>(smem);   // teams x D floats, parameters and ring done with
+    if constexpr (NORM) {
+      write_part(at, sa, out, buf);
+      write_part(at, sb, out + a.D, buf);
+      out += 2 * (int64_t)a.D;
+    }
+    if constexpr (BRANCH) {
+      write_part(at, s1, out, buf);
+      write_part(at, s0, out + a.D, buf);
+    }
+  }
+}
+
+struct FinalArgs {
+  const float* part;
+  int D, groups, parts, vecs, norm, branch;
+  const float *wp, *bp, *gv;
+  int gate_batch;
+  float *dgate, *dwp, *dbp, *dw, *db;
+};
+
+// Adds the CTAs' rows, in order. Block (x, y): 32 features, y = 0 the norm's
+// pair, y = 1 the branch's; warp w of 32 adds rows w, w + 32, ... of a group,
+// then warp 0 adds the warps' sums.
+__global__ void __launch_bounds__(1024) sub_final_kernel(const FinalArgs a) {
+  __shared__ float buf[2][32][33];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  const bool on = c < a.D;
+  const bool branch = a.norm ? blockIdx.y == 1 : true;
+  const int v0 = branch && a.norm ? 2 : 0;
+  float t1 = 0.f, t0 = 0.f;   // warp 0: totals over the groups
+  for (int g = 0; g < a.groups; ++g) {
+    float s1 = 0.f, s0 = 0.f;
+    if (on) {
+      for (int p = w; p < a.parts; p += 32) {
+        const float* r = a.part + ((int64_t)(g * (int64_t)a.parts + p) * a.vecs + v0) * a.D + c;
+        s1 += __ldg(r);
+        s0 += __ldg(r + a.D);
+      }
+    }
+    buf[0][w][lane] = s1;
+    buf[1][w][lane] = s0;
+    __syncthreads();
+    if (w == 0 && on) {
+      s1 = s0 = 0.f;
+      for (int k = 0; k < 32; ++k) {
+        s1 += buf[0][k][lane];
+        s0 += buf[1][k][lane];
+      }
+      if (branch) {
+        const float gate = a.gv ? a.gv[(a.gate_batch ? (int64_t)g * a.D : 0) + c] : 1.f;
+        if (a.dgate && (a.gate_batch || a.groups == 1))
+          a.dgate[(int64_t)g * a.D + c] =
+              (a.wp ? a.wp[c] : 1.f) * s1 + (a.bp ? a.bp[c] * s0 : 0.f);
+        t1 = fmaf(gate, s1, t1);
+        t0 = fmaf(gate, s0, t0);
+      } else {
+        t1 += s1;
+        t0 += s0;
+      }
+    }
+    __syncthreads();
+  }
+  if (w == 0 && on) {
+    float* o1 = branch ? a.dwp : a.dw;
+    float* o0 = branch ? a.dbp : a.db;
+    if (o1) o1[c] = t1;
+    if (o0) o0[c] = t0;
+  }
+}
+
+template <class T, int V, int PER, int TEAM>
+cudaError_t run(const SubCall& c, const SubArgs& a, const SubShape& s, cudaStream_t st) {
+  auto fn = !c.branch ? sub_bwd_kernel<T, V, PER, TEAM, false, true>
+            : c.norm  ? sub_bwd_kernel<T, V, PER, TEAM, true, true>
+                      : sub_bwd_kernel<T, V, PER, TEAM, true, false>;
+  // the row of partial sums goes through the same memory
+  const int smem = std::max(s.smem, s.teams * a.D * 4);
+  if (smem > kSmemDefault) {
+    cudaError_t e =
+        cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerSm);
+    if (e != cudaSuccess) return e;
+  }
+  fn<<<(unsigned)((int64_t)s.groups * s.parts), s.threads, smem, st>>>(a);
+  note_launch();
+  return cudaGetLastError();
+}
+template <class T>
+cudaError_t run_type(const SubCall& c, const SubArgs& a, const SubShape& s, cudaStream_t st) {
+  if (s.wide)
+    return with_team(s.team, [&](auto t) {
+      return run<T, 16 / (int)sizeof(T), kBwdPer, t.value>(c, a, s, st);
+    });
+  return s.team == 32 ? run<T, 1, kNarrowPer, 32>(c, a, s, st)
+                      : run<T, 1, kNarrowPer, 0>(c, a, s, st);
+}
+
+}  // namespace
+
+size_t sub_bwd_ws_bytes(int B, int H, int L, int d, bool branch, bool gate_batch) {
+  // as many rows as any kernel of the calls writes
+  const int D = H * d, groups = gate_batch ? B : 1;
+  const int64_t tokens = gate_batch ? L : (int64_t)B * L;
+  const int64_t parts = std::min<int64_t>(tokens, std::max(1, kBwdParts / std::max(1, groups)));
+  return align_up((size_t)groups * parts * (branch ? 4 : 2) * D * 4, 256);
+}
+
+cudaError_t launch_sub_bwd(const SubCall& c, void* ws, cudaStream_t st) {
+  const bool norm = c.norm != LSH_NORM_NONE;
+  const int tensors = 2 * norm + (c.dy != nullptr) + c.branch + (c.gate == LSH_GATE_SIGMOID);
+  const SubShape s = sub_shape(c, {kBwdPer, tensors, norm + 2 * c.branch, 2});
+  SubArgs a = sub_args(c, s);
+  const bool sums = c.dgate || c.dwp || c.dbp || c.dw || c.db;
+  a.part = sums ? (float*)ws : nullptr;
+  if ((int64_t)c.B * c.L == 0 && !sums) return cudaSuccess;
+  if ((int64_t)c.B * c.L > 0) {
+    cudaError_t e;
+    e = c.dtype == LSH_BF16 ? run_type<__nv_bfloat16>(c, a, s, st) : run_type<float>(c, a, s, st);
+    if (e != cudaSuccess || !sums) return e;
+  }
+  FinalArgs f{};
+  f.part = a.part;
+  f.D = a.D, f.groups = s.groups, f.parts = s.parts;
+  f.norm = norm, f.branch = c.branch;
+  f.vecs = 2 * (f.norm + f.branch);
+  f.wp = c.wp, f.bp = c.bp, f.gv = a.gv, f.gate_batch = c.gate_batch;
+  f.dgate = c.dgate, f.dwp = c.dwp, f.dbp = c.dbp, f.dw = c.dw, f.db = c.db;
+  sub_final_kernel<<<dim3((unsigned)((a.D + 31) / 32), (unsigned)(f.norm + f.branch)), 1024, 0,
+                     st>>>(f);
+  note_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace lsh

@@ -141,19 +141,25 @@ struct Philox {
   }
 };
 
-// v[i] = kept ? v[i] * scale : 0 for the V features starting at feature c of
-// a row whose groups of 8 start at counter n0 (V = 8: c is a multiple of 8).
+// v[i] = kept ? v[i] * scale : 0 for the V features starting at feature c (a
+// multiple of V) of a row whose groups of 8 start at counter n0.
+// Lane x is kept when x >= t, t in 1 .. 65536, which is x 2^16 > t 2^16 - 1:
+// with that bound in 32 bits (t = 65536 keeps nothing) the high half of a word
+// is compared in place, its low half bits below the bound's.
 template <int V>
 __device__ __forceinline__ void drop(float (&v)[V], const Philox& rng, uint64_t n0, int c,
                                      uint32_t t, float scale) {
-  static_assert(V == 8 || V == 1, "a whole group or one element");
+  static_assert(V == 8 || V == 4 || V == 1, "a group, half of one, or one element");
   const uint4 r = rng(n0 + (uint32_t)c / 8);
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-  if constexpr (V == 8) {
+  if constexpr (V > 1) {
+    const uint32_t bound = (t << 16) - 1u;
+    const bool high = V == 4 && (c & 4);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t lane = (i & 1) ? w[i / 2] >> 16 : w[i / 2] & 0xffffu;
-      v[i] = lane >= t ? v[i] * scale : 0.f;
+    for (int i = 0; i < V; ++i) {
+      const uint32_t u = high ? w[(i / 2 + 2) & 3] : w[i / 2];
+      const uint32_t lane = (i & 1) ? u : u << 16;
+      v[i] = lane > bound ? v[i] * scale : 0.f;
     }
   } else {
     const int i = c & 7;
