@@ -21,7 +21,8 @@ struct DropArgs {
   int H, L, gpr, rows, tile;   // tile: rows of a CTA
   uint32_t t;
   float scale;
-  uint64_t seed, offset;
+  PhiloxKeys key;
+  uint64_t offset;
   const uint64_t* counter;
   int64_t slice0;
 };
@@ -29,7 +30,7 @@ struct DropArgs {
 // A CTA takes `tile` rows; vector j of them is row j / upr, feature j mod upr.
 template <class T, int V>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant__ DropArgs a) {
-  const Philox rng(a.seed, a.offset + (a.counter ? __ldg(a.counter) : 0));
+  const uint64_t offset = a.offset + (a.counter ? __ldg(a.counter) : 0);
   const int row0 = blockIdx.x * a.tile;
   const int n = min(a.tile, a.rows - row0) * (int)a.upr.d;
   for (int j0 = threadIdx.x; j0 < n; j0 += kThreads * kUnits) {
@@ -48,7 +49,7 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant
         const int b = (int)a.fh.div((uint32_t)s), h = s - b * a.H;
         r[k].load((const T*)a.x + (b * a.sx.b + h * a.sx.h + l * a.sx.l + c[k]));
         out[k] = b * a.sy.b + h * a.sy.h + l * a.sy.l + c[k];
-        ctr[k] = (uint64_t)(a.slice0 * a.L + row) * (uint32_t)a.gpr;
+        ctr[k] = (uint64_t)(a.slice0 * a.L + row) * (uint32_t)a.gpr + (uint32_t)c[k] / 8;
       }
     }
 #pragma unroll
@@ -56,7 +57,11 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant
       if (j0 + k * kThreads < n) {
         float v[V];
         r[k].get(v);
-        if (a.t) drop<V>(v, rng, ctr[k], c[k], a.t, a.scale);
+        if (a.t) {
+          drop<V>(v, philox(a.key, ctr[k], offset), c[k], a.t);
+#pragma unroll
+          for (int i = 0; i < V; ++i) v[i] *= a.scale;
+        }
         r[k].set(v);
         r[k].store((T*)a.y + out[k]);
       }
@@ -82,7 +87,7 @@ cudaError_t launch_dropout(const lsh_dropout_problem& q, uint32_t t, float scale
   a.H = q.H, a.L = q.L, a.gpr = (q.d + 7) / 8;
   a.rows = q.B * q.H * q.L;
   a.tile = std::max(1, kThreads * kUnits / (int)a.upr.d);
-  a.t = t, a.scale = scale, a.seed = seed, a.offset = offset, a.counter = counter;
+  a.t = t, a.scale = scale, a.key = PhiloxKeys(seed), a.offset = offset, a.counter = counter;
   a.slice0 = q.slice0;
   if (q.dtype == LSH_BF16) wide ? run<__nv_bfloat16, 8>(a, s) : run<__nv_bfloat16, 1>(a, s);
   else wide ? run<float, 8>(a, s) : run<float, 1>(a, s);

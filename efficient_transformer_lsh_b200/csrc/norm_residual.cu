@@ -1,0 +1,185 @@
+// Norms and the residual add: how a call is laid over the GPU, and the sum of
+// the backward's partial parameter gradients.
+#include "norm_residual.cuh"
+
+namespace lsh {
+
+SubShape sub_shape(const SubCall& c, const SubSize& z) {
+  SubShape s{};
+  const int D = c.H * c.d, esize = c.dtype == LSH_BF16 ? 2 : 4;
+  s.groups = c.gate_batch ? c.B : 1;
+  s.tokens = c.gate_batch ? c.L : c.B * c.L;
+  s.wide = c.wide;
+  for (const lsh_strides* t : {&c.sx, &c.sf, &c.sh})
+    if ((c.H - 1) * t->h + c.d > (int64_t)INT32_MAX) s.wide = false;
+  int ctas = z.ctas;
+  for (;;) {
+    const int per = s.wide ? z.per : kNarrowPer;
+    // threads of a token: a power of two up to a warp, then whole warps
+    s.team = (D + per - 1) / per;
+    if (s.team > 32) {
+      s.team = (s.team + 31) / 32 * 32;
+    } else if (s.wide) {
+      int n = 2;
+      while (n < s.team) n *= 2;
+      s.team = n;
+    } else {
+      s.team = 32;
+    }
+    s.teams = std::max(1, kTeamThreads / s.team);
+    s.threads = s.teams * s.team;
+    const int fixed = z.vecs * per * 4 * s.team + (s.team > 32 ? s.teams * 32 * kMaxWarps : 0);
+    s.stages = 1;
+    s.smem = fixed;
+    if (s.wide) {
+      const int stage = z.tensors * (s.team > 32 ? s.threads : kTeamThreads) * per * esize;
+      while (ctas > 1 && fixed + 2 * stage > kSmemPerSm / ctas - 1024) --ctas;
+      if (fixed + stage > kSmemPerSm / ctas - 1024) {
+        s.wide = false;
+        continue;
+      }
+      s.stages = std::min(kMaxStages, (kSmemPerSm / ctas - 1024 - fixed) / stage);
+      s.smem = fixed + s.stages * stage;
+    }
+    break;
+  }
+  const int64_t rows = ((int64_t)s.tokens + s.teams - 1) / s.teams;
+  s.parts = (int)std::min<int64_t>(rows, std::max(1, kSms * ctas / std::max(1, s.groups)));
+  return s;
+}
+
+SubArgs sub_args(const SubCall& c, const SubShape& s) {
+  SubArgs a{};
+  const int V = !s.wide ? 1 : c.dtype == LSH_BF16 ? 8 : 4;
+  a.x = c.x, a.f = c.f, a.dy = c.dy, a.dh = c.dh;
+  a.y = c.y, a.h = c.h, a.dx = c.dx, a.df = c.df, a.dz = c.dz;
+  a.wp = c.wp, a.bp = c.bp, a.w = c.w, a.b = c.b;
+  a.z = c.gate == LSH_GATE_SIGMOID ? c.gatep : nullptr;
+  a.gv = c.gate == LSH_GATE_VECTOR ? (const float*)c.gatep : nullptr;
+  a.sx = c.sx, a.sf = c.sf, a.sh = c.sh;
+  a.upr = FastDiv((uint32_t)(c.d / V));
+  a.fl = FastDiv((uint32_t)std::max(1, c.L));
+  a.H = c.H, a.L = c.L, a.D = c.H * c.d;
+  a.units = a.D / V;
+  a.gpr = (c.d + 7) / 8;
+  a.tokens = s.tokens, a.parts = s.parts;
+  a.team = s.team, a.teams = s.teams, a.stages = s.stages;
+  a.post = c.post, a.norm = c.norm, a.gate = c.gate, a.gate_batch = c.gate_batch;
+  a.eps_post = c.eps_post, a.eps = c.eps, a.alpha = c.alpha, a.beta = c.beta;
+  a.inv_d = 1.f / (float)a.D;
+  a.drop_t = c.drop_t, a.drop_scale = c.drop_scale;
+  a.key = PhiloxKeys(c.seed), a.offset = c.offset, a.counter = c.counter;
+  a.ctr_h = (uint64_t)c.L * a.gpr, a.ctr_b = c.H * a.ctr_h, a.ctr0 = c.slice0 * a.ctr_h;
+  return a;
+}
+
+cudaError_t launch_sub_fwd(const SubCall& c, cudaStream_t st) {
+  const SubShape s = sub_shape(c, {kFwdPer, 1 + c.branch + (c.gate == LSH_GATE_SIGMOID),
+                                   c.branch ? 4 : 2, c.branch ? 2 : 3});
+  const SubArgs a = sub_args(c, s);
+  return c.dtype == LSH_BF16 ? sub_fwd_type<__nv_bfloat16>(c, a, s, st)
+                             : sub_fwd_type<float>(c, a, s, st);
+}
+
+namespace {
+
+struct FinalArgs {
+  const float* part;
+  int D, groups, parts, vecs, norm, branch;
+  const float *wp, *bp, *gv;
+  int gate_batch;
+  float *dgate, *dwp, *dbp, *dw, *db;
+};
+
+// Adds the CTAs' rows, in order. Block (x, y): 32 features, y = 0 the norm's
+// pair, y = 1 the branch's; warp w of 32 adds rows w, w + 32, ... of a group,
+// then warp 0 adds the warps' sums.
+__global__ void __launch_bounds__(1024) sub_final_kernel(const FinalArgs a) {
+  __shared__ float buf[2][32][33];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  const bool on = c < a.D;
+  const bool branch = a.norm ? blockIdx.y == 1 : true;
+  const int v0 = branch && a.norm ? 2 : 0;
+  float t1 = 0.f, t0 = 0.f;   // warp 0: totals over the groups
+  for (int g = 0; g < a.groups; ++g) {
+    float s1 = 0.f, s0 = 0.f;
+    if (on) {
+      for (int p = w; p < a.parts; p += 32) {
+        const float* r = a.part + ((int64_t)(g * (int64_t)a.parts + p) * a.vecs + v0) * a.D + c;
+        s1 += __ldg(r);
+        s0 += __ldg(r + a.D);
+      }
+    }
+    buf[0][w][lane] = s1;
+    buf[1][w][lane] = s0;
+    __syncthreads();
+    if (w == 0 && on) {
+      s1 = s0 = 0.f;
+      for (int k = 0; k < 32; ++k) {
+        s1 += buf[0][k][lane];
+        s0 += buf[1][k][lane];
+      }
+      if (branch) {
+        const float gate = a.gv ? a.gv[(a.gate_batch ? (int64_t)g * a.D : 0) + c] : 1.f;
+        if (a.dgate && (a.gate_batch || a.groups == 1))
+          a.dgate[(int64_t)g * a.D + c] =
+              (a.wp ? a.wp[c] : 1.f) * s1 + (a.bp ? a.bp[c] * s0 : 0.f);
+        t1 = fmaf(gate, s1, t1);
+        t0 = fmaf(gate, s0, t0);
+      } else {
+        t1 += s1;
+        t0 += s0;
+      }
+    }
+    __syncthreads();
+  }
+  if (w == 0 && on) {
+    float* o1 = branch ? a.dwp : a.dw;
+    float* o0 = branch ? a.dbp : a.db;
+    if (o1) o1[c] = t1;
+    if (o0) o0[c] = t0;
+  }
+}
+
+}  // namespace
+
+size_t sub_bwd_ws_bytes(int B, int H, int L, int d, bool branch, bool gate_batch) {
+  // as many rows as any kernel of the calls writes
+  const int D = H * d, groups = gate_batch ? B : 1;
+  const int64_t tokens = gate_batch ? L : (int64_t)B * L;
+  const int64_t parts = std::min<int64_t>(tokens, std::max(1, kBwdParts / std::max(1, groups)));
+  return align_up((size_t)groups * parts * (branch ? 4 : 2) * D * 4, 256);
+}
+
+cudaError_t launch_sub_bwd(const SubCall& c, void* ws, cudaStream_t st) {
+  const bool norm = c.norm != LSH_NORM_NONE;
+  const int tensors = 2 * norm + (c.dy != nullptr) + c.branch + (c.gate == LSH_GATE_SIGMOID);
+  const SubShape s = sub_shape(c, {kBwdPer, tensors, norm + 2 * c.branch, 2});
+  SubArgs a = sub_args(c, s);
+  const bool sums = c.dgate || c.dwp || c.dbp || c.dw || c.db;
+  a.part = sums ? (float*)ws : nullptr;
+  if ((int64_t)c.B * c.L == 0 && !sums) return cudaSuccess;
+  if ((int64_t)c.B * c.L > 0) {
+    cudaError_t e;
+    if (c.dtype == LSH_BF16)
+      e = norm ? sub_bwd_type<__nv_bfloat16, true>(c, a, s, st)
+               : sub_bwd_type<__nv_bfloat16, false>(c, a, s, st);
+    else
+      e = norm ? sub_bwd_type<float, true>(c, a, s, st) : sub_bwd_type<float, false>(c, a, s, st);
+    if (e != cudaSuccess || !sums) return e;
+  }
+  FinalArgs f{};
+  f.part = a.part;
+  f.D = a.D, f.groups = s.groups, f.parts = s.parts;
+  f.norm = norm, f.branch = c.branch;
+  f.vecs = 2 * (f.norm + f.branch);
+  f.wp = c.wp, f.bp = c.bp, f.gv = a.gv, f.gate_batch = c.gate_batch;
+  f.dgate = c.dgate, f.dwp = c.dwp, f.dbp = c.dbp, f.dw = c.dw, f.db = c.db;
+  sub_final_kernel<<<dim3((unsigned)((a.D + 31) / 32), (unsigned)(f.norm + f.branch)), 1024, 0,
+                     st>>>(f);
+  note_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace lsh

@@ -58,9 +58,10 @@ struct SubArgs {
   float eps_post, eps, alpha, beta, inv_d;
   uint32_t drop_t;
   float drop_scale;
-  uint64_t seed, offset;
+  PhiloxKeys key;
+  uint64_t offset;
   const uint64_t* counter;
-  int64_t slice0;
+  uint64_t ctr0, ctr_b, ctr_h;   // dropout groups before the first row; of a batch; of a head
 };
 
 // ---- pairs of floats in one 64-bit register pair ----
@@ -241,14 +242,41 @@ struct Place {
     return b * s.b + l * s.l;
   }
 
-  // Sums of N values over the team, the same on each of its threads. `red`
-  // holds two buffers used in turn, so one barrier a call is enough.
+  // Sums of N values over the team, the same on each of its threads. Two or
+  // four values share one butterfly: the first one or two exchanges split the
+  // values between the halves (quarters) of the team instead of adding the
+  // same sums on both, 14 and 22 instructions a warp instead of 20 and 40.
+  // `red` holds two buffers used in turn, so one barrier a call is enough.
   template <int N>
   __device__ __forceinline__ void team_sum(float (&v)[N]) {
+    constexpr int W = kMulti ? 32 : TEAM;
+    const unsigned all = 0xffffffffu;
+    const int me = threadIdx.x & 31;
+    if constexpr (N == 4 && W >= 4) {
+      const bool up1 = me & (W / 2), up2 = me & (W / 4);
+      float x = up1 ? v[2] : v[0], y = up1 ? v[3] : v[1];
+      x += __shfl_xor_sync(all, up1 ? v[0] : v[2], W / 2);
+      y += __shfl_xor_sync(all, up1 ? v[1] : v[3], W / 2);
+      float z = up2 ? y : x;
+      z += __shfl_xor_sync(all, up2 ? x : y, W / 4);
 #pragma unroll
-    for (int o = (kMulti ? 32 : TEAM) / 2; o > 0; o >>= 1)
+      for (int o = W / 8; o > 0; o >>= 1) z += __shfl_xor_sync(all, z, o);
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+      for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(all, z, i * (W / 4), W);
+    } else if constexpr (N == 2 && W >= 8) {
+      const bool up1 = me & (W / 2);
+      float x = up1 ? v[1] : v[0];
+      x += __shfl_xor_sync(all, up1 ? v[0] : v[1], W / 2);
+#pragma unroll
+      for (int o = W / 4; o > 0; o >>= 1) x += __shfl_xor_sync(all, x, o);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) v[i] = __shfl_sync(all, x, i * (W / 2), W);
+    } else {
+#pragma unroll
+      for (int o = W / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(all, v[i], o);
+    }
     if constexpr (kMulti) {
       float* r = red + turn * (4 * kMaxWarps);
       turn ^= 1;
@@ -409,8 +437,9 @@ struct Place {
   }
 
   // ---- dropout: kept values times m, others 0 ----
-  __device__ __forceinline__ void drop_all(const Philox& rng, int b, int l, float m,
+  __device__ __forceinline__ void drop_all(uint64_t offset, int b, int l, float m,
                                            f2 (&v)[P]) const {
+    const uint64_t first = a.ctr0 + (uint32_t)b * a.ctr_b + (uint64_t)(uint32_t)l * (uint32_t)a.gpr;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       float e[V];
@@ -419,8 +448,9 @@ struct Place {
         const float2 u = up(v[(k * V + i) / 2]);
         e[i] = (k * V + i) & 1 ? u.y : u.x;
       }
-      const uint64_t row = (uint64_t)((a.slice0 + (int64_t)b * a.H + head(k)) * a.L + l);
-      drop<V>(e, rng, row * (uint32_t)a.gpr, col(k), a.drop_t, m);
+      const int c = col(k);
+      const uint64_t n = first + (uint32_t)head(k) * a.ctr_h + (uint32_t)c / 8;
+      drop<V>(e, philox(a.key, n, offset), c, a.drop_t);
       if constexpr (kRing) {
 #pragma unroll
         for (int i = 0; i < V / 2; ++i) v[V / 2 * k + i] = pk(e[2 * i], e[2 * i + 1]);
@@ -429,6 +459,7 @@ struct Place {
         v[k / 2] = k & 1 ? pk(u.x, e[0]) : pk(e[0], u.y);
       }
     }
+    scale_all(v, m);
   }
   // v - m on the features that exist, 0 elsewhere
   __device__ __forceinline__ void center(f2 (&v)[P], float m) const {
@@ -482,6 +513,13 @@ cudaError_t with_team(int team, F f) {
     default: return f(std::integral_constant<int, 0>());
   }
 }
+
+constexpr int kFwdPer = 32, kBwdPer = 16;   // features a thread of the wide kernels
+
+template <class T>
+cudaError_t sub_fwd_type(const SubCall& c, const SubArgs& a, const SubShape& s, cudaStream_t st);
+template <class T, bool NORM>
+cudaError_t sub_bwd_type(const SubCall& c, const SubArgs& a, const SubShape& s, cudaStream_t st);
 
 // Rows of partial sums a backward call may write (of any kernel).
 constexpr int kBwdParts = 2 * kSms;

@@ -1,4 +1,6 @@
-// Backward of the norms and the residual add; see norm_residual.cuh.
+// Backward kernel of the norms and the residual add; see norm_residual.cuh.
+// Instantiated for each element type, with and without a norm of y, in a file
+// of its own.
 //
 // Parameter gradients are sums over tokens. Every thread keeps its features'
 // sums in registers over all the tokens it visits; a CTA writes one row of
@@ -13,12 +15,12 @@
 // deviations of y and f, a and a (y - mean) together (a does not depend on the
 // statistics, so r is factored out: mean(a yhat) = r mean(a (y - mean))); then
 // the second norm's a and a (f - mean).
+#pragma once
+
 #include "norm_residual.cuh"
 
 namespace lsh {
 namespace {
-
-constexpr int kBwdPer = 16;   // features a thread
 
 // A CTA's row of partial sums: the teams' sums are added in order.
 template <class At>
@@ -45,7 +47,7 @@ __device__ __forceinline__ void write_part(const At& at, const f2 (&s)[At::P], f
 
 // Parameters, in order: W, P1 = gate w_post (a sigmoid gate is not in it), P0
 // = b_post (sigmoid gates only).
-template <class T, int V, int PER, int TEAM, bool BRANCH, bool NORM>
+template <class T, int V, int PER, int TEAM, bool BRANCH, bool NORM, bool POST, bool SIG>
 __global__ void __launch_bounds__(TEAM == 0 ? 32 * kMaxWarps : kTeamThreads, TEAM == 0 ? 1 : 2)
 sub_bwd_kernel(const __grid_constant__ SubArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
@@ -53,11 +55,10 @@ sub_bwd_kernel(const __grid_constant__ SubArgs a) {
   constexpr int P = At::P;
   constexpr int kP1 = NORM ? 1 : 0, kP0 = kP1 + 1;
   At at(a, smem);
-  const bool post = BRANCH && a.post != LSH_NORM_NONE;
-  const bool sig = BRANCH && a.gate == LSH_GATE_SIGMOID;
+  constexpr bool post = BRANCH && POST, sig = BRANCH && SIG;
   const float* gv = a.gv ? a.gv + (int64_t)at.group * (a.gate_batch ? a.D : 0) : nullptr;
   const bool has1 = BRANCH && (a.wp || gv), has0 = sig && a.bp;
-  if (NORM && a.w) at.stage_param(0, a.w, nullptr);
+  if (NORM) at.stage_param(0, a.w, nullptr);
   if (has1) at.stage_param(kP1, a.wp, gv);
   if (has0) at.stage_param(kP0, a.bp, nullptr);
   // the ring's tensors: y dh, dy, f, z
@@ -65,7 +66,7 @@ sub_bwd_kernel(const __grid_constant__ SubArgs a) {
   const int tensors = i_f + BRANCH + sig;
   at.clear(at.ring, a.stages * tensors);
   __syncthreads();
-  const Philox rng(a.seed, a.offset + (a.counter ? __ldg(a.counter) : 0));
+  const uint64_t offset = a.offset + (a.counter ? __ldg(a.counter) : 0);
   const int step = at.step(), rounds = at.rounds();
   const uint32_t one = at.tensor();
   const uint32_t stage_bytes = tensors * one;
@@ -143,14 +144,14 @@ sub_bwd_kernel(const __grid_constant__ SubArgs a) {
       at.get(a.dh, a.sh, b, l, live, st + one, q);
 #pragma unroll
       for (int i = 0; i < P; ++i) sb[i] = add2(sb[i], q[i]);
-      if (a.w) at.scale_by(0, q);
+      at.scale_by(0, q);
       s[1] = sum_all(q);
       s[2] = dot_all(q, hat);
       at.team_sum(s);
       const float r = inv_std(s[0], a.inv_d, a.eps);
       if (post) r_f = inv_std(s[3], a.inv_d, a.eps_post);
       const float m0 = ly ? s[1] * a.inv_d : 0.f, m1 = r * r * s[2] * a.inv_d;
-      const f2 r2 = pk(r, r), nm0 = pk(-m0, -m0), nm1 = pk(-m1, -m1);
+      const f2 r2 = pk(r, r), k0 = pk(-r * m0, -r * m0), k1 = pk(-r * m1, -r * m1);
       {
         f2 dh[P];
         at.get(a.dh, a.sh, b, l, live, st + one, dh);
@@ -158,7 +159,7 @@ sub_bwd_kernel(const __grid_constant__ SubArgs a) {
         for (int i = 0; i < P; ++i) sa[i] = fma2(dh[i], mul2(hat[i], r2), sa[i]);
       }
 #pragma unroll
-      for (int i = 0; i < P; ++i) q[i] = mul2(r2, fma2(hat[i], nm1, add2(q[i], nm0)));
+      for (int i = 0; i < P; ++i) q[i] = fma2(q[i], r2, fma2(hat[i], k1, k0));
       if (a.dy) {
         f2 dy[P];
         at.get(a.dy, a.sx, b, l, live, st + i_dy * one, dy);
@@ -193,7 +194,7 @@ sub_bwd_kernel(const __grid_constant__ SubArgs a) {
         }
         scale_all(hat, r_f);
       }
-      if (a.drop_t) at.drop_all(rng, b, l, a.alpha * a.drop_scale, q);
+      if (a.drop_t) at.drop_all(offset, b, l, a.alpha * a.drop_scale, q);
       else scale_all(q, a.alpha);
       if (sig) {
         f2 u[P], z[P];
@@ -222,9 +223,9 @@ sub_bwd_kernel(const __grid_constant__ SubArgs a) {
         float s[2] = {sum_all(q), dot_all(q, hat)};
         at.team_sum(s);
         const float m0 = a.post == LSH_NORM_LAYER ? s[0] * a.inv_d : 0.f, m1 = s[1] * a.inv_d;
-        const f2 r2 = pk(r_f, r_f), nm0 = pk(-m0, -m0), nm1 = pk(-m1, -m1);
+        const f2 r2 = pk(r_f, r_f), k0 = pk(-r_f * m0, -r_f * m0), k1 = pk(-r_f * m1, -r_f * m1);
 #pragma unroll
-        for (int i = 0; i < P; ++i) q[i] = mul2(r2, fma2(hat[i], nm1, add2(q[i], nm0)));
+        for (int i = 0; i < P; ++i) q[i] = fma2(q[i], r2, fma2(hat[i], k1, k0));
       }
       at.template put<false>(a.df, a.sf, at.of, b, l, live, q);
     }
@@ -248,70 +249,15 @@ sub_bwd_kernel(const __grid_constant__ SubArgs a) {
   }
 }
 
-struct FinalArgs {
-  const float* part;
-  int D, groups, parts, vecs, norm, branch;
-  const float *wp, *bp, *gv;
-  int gate_batch;
-  float *dgate, *dwp, *dbp, *dw, *db;
-};
-
-// Adds the CTAs' rows, in order. Block (x, y): 32 features, y = 0 the norm's
-// pair, y = 1 the branch's; warp w of 32 adds rows w, w + 32, ... of a group,
-// then warp 0 adds the warps' sums.
-__global__ void __launch_bounds__(1024) sub_final_kernel(const FinalArgs a) {
-  __shared__ float buf[2][32][33];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
-  const bool on = c < a.D;
-  const bool branch = a.norm ? blockIdx.y == 1 : true;
-  const int v0 = branch && a.norm ? 2 : 0;
-  float t1 = 0.f, t0 = 0.f;   // warp 0: totals over the groups
-  for (int g = 0; g < a.groups; ++g) {
-    float s1 = 0.f, s0 = 0.f;
-    if (on) {
-      for (int p = w; p < a.parts; p += 32) {
-        const float* r = a.part + ((int64_t)(g * (int64_t)a.parts + p) * a.vecs + v0) * a.D + c;
-        s1 += __ldg(r);
-        s0 += __ldg(r + a.D);
-      }
-    }
-    buf[0][w][lane] = s1;
-    buf[1][w][lane] = s0;
-    __syncthreads();
-    if (w == 0 && on) {
-      s1 = s0 = 0.f;
-      for (int k = 0; k < 32; ++k) {
-        s1 += buf[0][k][lane];
-        s0 += buf[1][k][lane];
-      }
-      if (branch) {
-        const float gate = a.gv ? a.gv[(a.gate_batch ? (int64_t)g * a.D : 0) + c] : 1.f;
-        if (a.dgate && (a.gate_batch || a.groups == 1))
-          a.dgate[(int64_t)g * a.D + c] =
-              (a.wp ? a.wp[c] : 1.f) * s1 + (a.bp ? a.bp[c] * s0 : 0.f);
-        t1 = fmaf(gate, s1, t1);
-        t0 = fmaf(gate, s0, t0);
-      } else {
-        t1 += s1;
-        t0 += s0;
-      }
-    }
-    __syncthreads();
-  }
-  if (w == 0 && on) {
-    float* o1 = branch ? a.dwp : a.dw;
-    float* o0 = branch ? a.dbp : a.db;
-    if (o1) o1[c] = t1;
-    if (o0) o0[c] = t0;
-  }
-}
-
-template <class T, int V, int PER, int TEAM>
-cudaError_t run(const SubCall& c, const SubArgs& a, const SubShape& s, cudaStream_t st) {
-  auto fn = !c.branch ? sub_bwd_kernel<T, V, PER, TEAM, false, true>
-            : c.norm  ? sub_bwd_kernel<T, V, PER, TEAM, true, true>
-                      : sub_bwd_kernel<T, V, PER, TEAM, true, false>;
+template <class T, int V, int PER, int TEAM, bool NORM>
+cudaError_t run_branch(const SubCall& c, const SubArgs& a, const SubShape& s, cudaStream_t st) {
+  const bool sig = c.gate == LSH_GATE_SIGMOID, post = c.post != LSH_NORM_NONE;
+  auto fn = post && sig ? sub_bwd_kernel<T, V, PER, TEAM, true, NORM, true, true>
+            : post      ? sub_bwd_kernel<T, V, PER, TEAM, true, NORM, true, false>
+            : sig       ? sub_bwd_kernel<T, V, PER, TEAM, true, NORM, false, true>
+                        : sub_bwd_kernel<T, V, PER, TEAM, true, NORM, false, false>;
+  if constexpr (NORM)
+    if (!c.branch) fn = sub_bwd_kernel<T, V, PER, TEAM, false, true, false, false>;
   // the row of partial sums goes through the same memory
   const int smem = std::max(s.smem, s.teams * a.D * 4);
   if (smem > kSmemDefault) {
@@ -323,50 +269,17 @@ cudaError_t run(const SubCall& c, const SubArgs& a, const SubShape& s, cudaStrea
   note_launch();
   return cudaGetLastError();
 }
-template <class T>
-cudaError_t run_type(const SubCall& c, const SubArgs& a, const SubShape& s, cudaStream_t st) {
-  if (s.wide)
-    return with_team(s.team, [&](auto t) {
-      return run<T, 16 / (int)sizeof(T), kBwdPer, t.value>(c, a, s, st);
-    });
-  return s.team == 32 ? run<T, 1, kNarrowPer, 32>(c, a, s, st)
-                      : run<T, 1, kNarrowPer, 0>(c, a, s, st);
-}
 
 }  // namespace
 
-size_t sub_bwd_ws_bytes(int B, int H, int L, int d, bool branch, bool gate_batch) {
-  // as many rows as any kernel of the calls writes
-  const int D = H * d, groups = gate_batch ? B : 1;
-  const int64_t tokens = gate_batch ? L : (int64_t)B * L;
-  const int64_t parts = std::min<int64_t>(tokens, std::max(1, kBwdParts / std::max(1, groups)));
-  return align_up((size_t)groups * parts * (branch ? 4 : 2) * D * 4, 256);
-}
-
-cudaError_t launch_sub_bwd(const SubCall& c, void* ws, cudaStream_t st) {
-  const bool norm = c.norm != LSH_NORM_NONE;
-  const int tensors = 2 * norm + (c.dy != nullptr) + c.branch + (c.gate == LSH_GATE_SIGMOID);
-  const SubShape s = sub_shape(c, {kBwdPer, tensors, norm + 2 * c.branch, 2});
-  SubArgs a = sub_args(c, s);
-  const bool sums = c.dgate || c.dwp || c.dbp || c.dw || c.db;
-  a.part = sums ? (float*)ws : nullptr;
-  if ((int64_t)c.B * c.L == 0 && !sums) return cudaSuccess;
-  if ((int64_t)c.B * c.L > 0) {
-    cudaError_t e;
-    e = c.dtype == LSH_BF16 ? run_type<__nv_bfloat16>(c, a, s, st) : run_type<float>(c, a, s, st);
-    if (e != cudaSuccess || !sums) return e;
-  }
-  FinalArgs f{};
-  f.part = a.part;
-  f.D = a.D, f.groups = s.groups, f.parts = s.parts;
-  f.norm = norm, f.branch = c.branch;
-  f.vecs = 2 * (f.norm + f.branch);
-  f.wp = c.wp, f.bp = c.bp, f.gv = a.gv, f.gate_batch = c.gate_batch;
-  f.dgate = c.dgate, f.dwp = c.dwp, f.dbp = c.dbp, f.dw = c.dw, f.db = c.db;
-  sub_final_kernel<<<dim3((unsigned)((a.D + 31) / 32), (unsigned)(f.norm + f.branch)), 1024, 0,
-                     st>>>(f);
-  note_launch();
-  return cudaGetLastError();
+template <class T, bool NORM>
+cudaError_t sub_bwd_type(const SubCall& c, const SubArgs& a, const SubShape& s, cudaStream_t st) {
+  if (s.wide)
+    return with_team(s.team, [&](auto t) {
+      return run_branch<T, 16 / (int)sizeof(T), kBwdPer, t.value, NORM>(c, a, s, st);
+    });
+  return s.team == 32 ? run_branch<T, 1, kNarrowPer, 32, NORM>(c, a, s, st)
+                      : run_branch<T, 1, kNarrowPer, 0, NORM>(c, a, s, st);
 }
 
 }  // namespace lsh

@@ -1,4 +1,7 @@
-// Forward of the norms and the residual add; see norm_residual.cuh.
+// Forward kernel of the norms and the residual add; see norm_residual.cuh.
+// Instantiated for each element type in a file of its own.
+#pragma once
+
 #include "norm_residual.cuh"
 
 namespace lsh {
@@ -6,15 +9,15 @@ namespace {
 
 // Parameters, in order: P1 = gate w_post, P0 = gate b_post (a sigmoid gate is
 // not in them), W, B: the products are formed once a CTA, not once a token.
-template <class T, int V, int PER, int TEAM, bool BRANCH>
+template <class T, int V, int PER, int TEAM, bool BRANCH, bool POST, bool SIG>
 __global__ void __launch_bounds__(V == 1 ? 32 * kMaxWarps : kTeamThreads)
 sub_fwd_kernel(const __grid_constant__ SubArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   using At = Place<T, V, PER, TEAM, BRANCH ? 4 : 2>;
   constexpr int P = At::P;
   At at(a, smem);
-  const bool post = BRANCH && a.post != LSH_NORM_NONE, norm = a.norm != LSH_NORM_NONE;
-  const bool sig = BRANCH && a.gate == LSH_GATE_SIGMOID;
+  constexpr bool post = BRANCH && POST, sig = BRANCH && SIG;
+  const bool norm = a.norm != LSH_NORM_NONE;
   const float* gv = a.gv ? a.gv + (int64_t)at.group * (a.gate_batch ? a.D : 0) : nullptr;
   const bool has1 = BRANCH && (a.wp || gv), has0 = BRANCH && a.bp;
   constexpr int kW = BRANCH ? 2 : 0, kB = kW + 1;
@@ -25,7 +28,7 @@ sub_fwd_kernel(const __grid_constant__ SubArgs a) {
   const int tensors = 1 + BRANCH + sig;
   at.clear(at.ring, a.stages * tensors);
   __syncthreads();
-  const Philox rng(a.seed, a.offset + (a.counter ? __ldg(a.counter) : 0));
+  const uint64_t offset = a.offset + (a.counter ? __ldg(a.counter) : 0);
   const int step = at.step(), rounds = at.rounds();
   const uint32_t stage_bytes = tensors * at.tensor();
 
@@ -91,7 +94,7 @@ sub_fwd_kernel(const __grid_constant__ SubArgs a) {
       }
       float m = a.alpha;
       if (a.drop_t) {
-        at.drop_all(rng, b, l, m * a.drop_scale, v);
+        at.drop_all(offset, b, l, m * a.drop_scale, v);
         m = 1.f;
       }
       f2 x[P];
@@ -127,8 +130,12 @@ sub_fwd_kernel(const __grid_constant__ SubArgs a) {
 
 template <class T, int V, int PER, int TEAM>
 cudaError_t run(const SubCall& c, const SubArgs& a, const SubShape& s, cudaStream_t st) {
-  auto fn = c.branch ? sub_fwd_kernel<T, V, PER, TEAM, true>
-                     : sub_fwd_kernel<T, V, PER, TEAM, false>;
+  const bool sig = c.gate == LSH_GATE_SIGMOID, post = c.post != LSH_NORM_NONE;
+  auto fn = !c.branch     ? sub_fwd_kernel<T, V, PER, TEAM, false, false, false>
+            : post && sig ? sub_fwd_kernel<T, V, PER, TEAM, true, true, true>
+            : post        ? sub_fwd_kernel<T, V, PER, TEAM, true, true, false>
+            : sig         ? sub_fwd_kernel<T, V, PER, TEAM, true, false, true>
+                          : sub_fwd_kernel<T, V, PER, TEAM, true, false, false>;
   if (s.smem > kSmemDefault) {
     cudaError_t e =
         cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerSm);
@@ -138,91 +145,17 @@ cudaError_t run(const SubCall& c, const SubArgs& a, const SubShape& s, cudaStrea
   note_launch();
   return cudaGetLastError();
 }
-template <class T>
-cudaError_t run_type(const SubCall& c, const SubArgs& a, const SubShape& s, cudaStream_t st) {
-  if (s.wide)
-    return with_team(s.team, [&](auto t) {
-      return run<T, 16 / (int)sizeof(T), 32, t.value>(c, a, s, st);
-    });
-  return s.team == 32 ? run<T, 1, kNarrowPer, 32>(c, a, s, st)
-                      : run<T, 1, kNarrowPer, 0>(c, a, s, st);
-}
 
 }  // namespace
 
-SubShape sub_shape(const SubCall& c, const SubSize& z) {
-  SubShape s{};
-  const int D = c.H * c.d, esize = c.dtype == LSH_BF16 ? 2 : 4;
-  s.groups = c.gate_batch ? c.B : 1;
-  s.tokens = c.gate_batch ? c.L : c.B * c.L;
-  s.wide = c.wide;
-  for (const lsh_strides* t : {&c.sx, &c.sf, &c.sh})
-    if ((c.H - 1) * t->h + c.d > (int64_t)INT32_MAX) s.wide = false;
-  int ctas = z.ctas;
-  for (;;) {
-    const int per = s.wide ? z.per : kNarrowPer;
-    // threads of a token: a power of two up to a warp, then whole warps
-    s.team = (D + per - 1) / per;
-    if (s.team > 32) {
-      s.team = (s.team + 31) / 32 * 32;
-    } else if (s.wide) {
-      int n = 2;
-      while (n < s.team) n *= 2;
-      s.team = n;
-    } else {
-      s.team = 32;
-    }
-    s.teams = std::max(1, kTeamThreads / s.team);
-    s.threads = s.teams * s.team;
-    const int fixed = z.vecs * per * 4 * s.team + (s.team > 32 ? s.teams * 32 * kMaxWarps : 0);
-    s.stages = 1;
-    s.smem = fixed;
-    if (s.wide) {
-      const int stage = z.tensors * (s.team > 32 ? s.threads : kTeamThreads) * per * esize;
-      while (ctas > 1 && fixed + 2 * stage > kSmemPerSm / ctas - 1024) --ctas;
-      if (fixed + stage > kSmemPerSm / ctas - 1024) {
-        s.wide = false;
-        continue;
-      }
-      s.stages = std::min(kMaxStages, (kSmemPerSm / ctas - 1024 - fixed) / stage);
-      s.smem = fixed + s.stages * stage;
-    }
-    break;
-  }
-  const int64_t rows = ((int64_t)s.tokens + s.teams - 1) / s.teams;
-  s.parts = (int)std::min<int64_t>(rows, std::max(1, kSms * ctas / std::max(1, s.groups)));
-  return s;
-}
-
-SubArgs sub_args(const SubCall& c, const SubShape& s) {
-  SubArgs a{};
-  const int V = !s.wide ? 1 : c.dtype == LSH_BF16 ? 8 : 4;
-  a.x = c.x, a.f = c.f, a.dy = c.dy, a.dh = c.dh;
-  a.y = c.y, a.h = c.h, a.dx = c.dx, a.df = c.df, a.dz = c.dz;
-  a.wp = c.wp, a.bp = c.bp, a.w = c.w, a.b = c.b;
-  a.z = c.gate == LSH_GATE_SIGMOID ? c.gatep : nullptr;
-  a.gv = c.gate == LSH_GATE_VECTOR ? (const float*)c.gatep : nullptr;
-  a.sx = c.sx, a.sf = c.sf, a.sh = c.sh;
-  a.upr = FastDiv((uint32_t)(c.d / V));
-  a.fl = FastDiv((uint32_t)std::max(1, c.L));
-  a.H = c.H, a.L = c.L, a.D = c.H * c.d;
-  a.units = a.D / V;
-  a.gpr = (c.d + 7) / 8;
-  a.tokens = s.tokens, a.parts = s.parts;
-  a.team = s.team, a.teams = s.teams, a.stages = s.stages;
-  a.post = c.post, a.norm = c.norm, a.gate = c.gate, a.gate_batch = c.gate_batch;
-  a.eps_post = c.eps_post, a.eps = c.eps, a.alpha = c.alpha, a.beta = c.beta;
-  a.inv_d = 1.f / (float)a.D;
-  a.drop_t = c.drop_t, a.drop_scale = c.drop_scale;
-  a.seed = c.seed, a.offset = c.offset, a.counter = c.counter, a.slice0 = c.slice0;
-  return a;
-}
-
-cudaError_t launch_sub_fwd(const SubCall& c, cudaStream_t st) {
-  const SubShape s = sub_shape(c, {32, 1 + c.branch + (c.gate == LSH_GATE_SIGMOID),
-                                   c.branch ? 4 : 2, c.branch ? 2 : 3});
-  const SubArgs a = sub_args(c, s);
-  return c.dtype == LSH_BF16 ? run_type<__nv_bfloat16>(c, a, s, st) : run_type<float>(c, a, s, st);
+template <class T>
+cudaError_t sub_fwd_type(const SubCall& c, const SubArgs& a, const SubShape& s, cudaStream_t st) {
+  if (s.wide)
+    return with_team(s.team, [&](auto t) {
+      return run<T, 16 / (int)sizeof(T), kFwdPer, t.value>(c, a, s, st);
+    });
+  return s.team == 32 ? run<T, 1, kNarrowPer, 32>(c, a, s, st)
+                      : run<T, 1, kNarrowPer, 0>(c, a, s, st);
 }
 
 }  // namespace lsh

@@ -119,38 +119,42 @@ struct FastDiv {
 };
 
 // Ten rounds of Philox4x32 (Salmon et al., SC 2011): two 32 x 32 -> 64-bit
-// products a round, keys stepped by two odd constants.
-struct Philox {
-  uint32_t k0, k1, c2, c3;
-  __device__ __forceinline__ Philox(uint64_t seed, uint64_t offset)
-      : k0((uint32_t)seed), k1((uint32_t)(seed >> 32)), c2((uint32_t)offset),
-        c3((uint32_t)(offset >> 32)) {}
-  __device__ __forceinline__ uint4 operator()(uint64_t n) const {
-    uint32_t x0 = (uint32_t)n, x1 = (uint32_t)(n >> 32), x2 = c2, x3 = c3, a = k0, b = k1;
-#pragma unroll
+// products a round, keys stepped by two odd constants. The round keys are a
+// function of the seed alone, formed on the host, so that they are constant
+// operands of the exclusive-ors.
+struct PhiloxKeys {
+  uint32_t k0[10], k1[10];
+  PhiloxKeys() = default;
+  explicit PhiloxKeys(uint64_t seed) {
+    uint32_t a = (uint32_t)seed, b = (uint32_t)(seed >> 32);
     for (int r = 0; r < 10; ++r) {
-      const uint64_t p = (uint64_t)x0 * 0xD2511F53u, q = (uint64_t)x2 * 0xCD9E8D57u;
-      x0 = (uint32_t)(q >> 32) ^ x1 ^ a;
-      x1 = (uint32_t)q;
-      x2 = (uint32_t)(p >> 32) ^ x3 ^ b;
-      x3 = (uint32_t)p;
-      a += 0x9E3779B9u;
-      b += 0xBB67AE85u;
+      k0[r] = a, k1[r] = b;
+      a += 0x9E3779B9u, b += 0xBB67AE85u;
     }
-    return make_uint4(x0, x1, x2, x3);
   }
 };
+__device__ __forceinline__ uint4 philox(const PhiloxKeys& key, uint64_t n, uint64_t offset) {
+  uint32_t x0 = (uint32_t)n, x1 = (uint32_t)(n >> 32), x2 = (uint32_t)offset,
+           x3 = (uint32_t)(offset >> 32);
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+    const uint64_t p = (uint64_t)x0 * 0xD2511F53u, q = (uint64_t)x2 * 0xCD9E8D57u;
+    x0 = (uint32_t)(q >> 32) ^ x1 ^ key.k0[r];
+    x1 = (uint32_t)q;
+    x2 = (uint32_t)(p >> 32) ^ x3 ^ key.k1[r];
+    x3 = (uint32_t)p;
+  }
+  return make_uint4(x0, x1, x2, x3);
+}
 
-// v[i] = kept ? v[i] * scale : 0 for the V features starting at feature c (a
-// multiple of V) of a row whose groups of 8 start at counter n0.
+// v[i] = kept ? v[i] : 0 for the V features starting at feature c (a multiple
+// of V) of a row, r being the random words of the group of 8 that c is in.
 // Lane x is kept when x >= t, t in 1 .. 65536, which is x 2^16 > t 2^16 - 1:
 // with that bound in 32 bits (t = 65536 keeps nothing) the high half of a word
 // is compared in place, its low half bits below the bound's.
 template <int V>
-__device__ __forceinline__ void drop(float (&v)[V], const Philox& rng, uint64_t n0, int c,
-                                     uint32_t t, float scale) {
+__device__ __forceinline__ void drop(float (&v)[V], const uint4& r, int c, uint32_t t) {
   static_assert(V == 8 || V == 4 || V == 1, "a group, half of one, or one element");
-  const uint4 r = rng(n0 + (uint32_t)c / 8);
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
   if constexpr (V > 1) {
     const uint32_t bound = (t << 16) - 1u;
@@ -159,13 +163,13 @@ __device__ __forceinline__ void drop(float (&v)[V], const Philox& rng, uint64_t 
     for (int i = 0; i < V; ++i) {
       const uint32_t u = high ? w[(i / 2 + 2) & 3] : w[i / 2];
       const uint32_t lane = (i & 1) ? u : u << 16;
-      v[i] = lane > bound ? v[i] * scale : 0.f;
+      v[i] = lane > bound ? v[i] : 0.f;
     }
   } else {
     const int i = c & 7;
     const uint32_t u = (i & 4) ? ((i & 2) ? w[3] : w[2]) : ((i & 2) ? w[1] : w[0]);
     const uint32_t lane = (i & 1) ? u >> 16 : u & 0xffffu;
-    v[0] = lane >= t ? v[0] * scale : 0.f;
+    v[0] = lane >= t ? v[0] : 0.f;
   }
 }
 
