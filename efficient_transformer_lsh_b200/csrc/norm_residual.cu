@@ -4,6 +4,9 @@
 
 namespace lsh {
 
+// CTAs of a group when `all` share the groups.
+static int max_parts(int all, int groups) { return std::max(1, all / std::max(1, groups)); }
+
 SubShape sub_shape(const SubCall& c, const SubSize& z) {
   SubShape s{};
   const int D = c.H * c.d, esize = c.dtype == LSH_BF16 ? 2 : 4;
@@ -12,9 +15,10 @@ SubShape sub_shape(const SubCall& c, const SubSize& z) {
   s.wide = c.wide;
   for (const lsh_strides* t : {&c.sx, &c.sf, &c.sh})
     if ((c.H - 1) * t->h + c.d > (int64_t)INT32_MAX) s.wide = false;
-  int ctas = z.ctas;
+  int ctas;
   for (;;) {
-    const int per = s.wide ? z.per : kNarrowPer;
+    const int per = s.wide ? z.per : kNarrowPer, threads = s.wide ? z.threads : kNarrowThreads;
+    s.tok = s.wide ? z.tok : 1;
     // threads of a token: a power of two up to a warp, then whole warps
     s.team = (D + per - 1) / per;
     if (s.team > 32) {
@@ -26,13 +30,23 @@ SubShape sub_shape(const SubCall& c, const SubSize& z) {
     } else {
       s.team = 32;
     }
-    s.teams = std::max(1, kTeamThreads / s.team);
+    // Teams of several warps: two tokens at a time halve the barriers, which
+    // pays where a branch makes many (4 x 4096 x 4096, everything on: 238 us
+    // against 307), but a norm alone gains more from twice the warps (196
+    // against 247); 512 threads of two tokens do not fit the register file.
+    if (s.team > 256 || (s.team > 32 && !c.branch)) s.tok = 1;
+    s.teams = std::max(1, threads / s.team);
     s.threads = s.teams * s.team;
-    const int fixed = z.vecs * per * 4 * s.team + (s.team > 32 ? s.teams * 32 * kMaxWarps : 0);
+    // threads resident on an SM, by the registers of each form
+    int room = 512;
+    if (s.wide && s.team > 32 && z.tok > 1) room = s.tok > 1 ? 256 : 512;
+    else if (s.wide) room = z.ctas * threads;
+    ctas = std::max(1, room / s.threads);
+    const int fixed = z.vecs * per * 4 * s.team + (s.team > 32 ? s.teams * 64 * kMaxWarps : 0);
     s.stages = 1;
     s.smem = fixed;
     if (s.wide) {
-      const int stage = z.tensors * (s.team > 32 ? s.threads : kTeamThreads) * per * esize;
+      const int stage = z.tensors * s.tok * (s.team > 32 ? s.threads : threads) * per * esize;
       while (ctas > 1 && fixed + 2 * stage > kSmemPerSm / ctas - 1024) --ctas;
       if (fixed + stage > kSmemPerSm / ctas - 1024) {
         s.wide = false;
@@ -43,8 +57,8 @@ SubShape sub_shape(const SubCall& c, const SubSize& z) {
     }
     break;
   }
-  const int64_t rows = ((int64_t)s.tokens + s.teams - 1) / s.teams;
-  s.parts = (int)std::min<int64_t>(rows, std::max(1, kSms * ctas / std::max(1, s.groups)));
+  const int64_t rows = ((int64_t)s.tokens + s.teams * s.tok - 1) / (s.teams * s.tok);
+  s.parts = (int)std::min<int64_t>(rows, max_parts(std::min(kSms * ctas, kMaxParts), s.groups));
   return s;
 }
 
@@ -74,8 +88,9 @@ SubArgs sub_args(const SubCall& c, const SubShape& s) {
 }
 
 cudaError_t launch_sub_fwd(const SubCall& c, cudaStream_t st) {
-  const SubShape s = sub_shape(c, {kFwdPer, 1 + c.branch + (c.gate == LSH_GATE_SIGMOID),
-                                   c.branch ? 4 : 2, c.branch ? 2 : 3});
+  const SubShape s = sub_shape(c, {kFwdPer, 1, kFwdThreads,
+                                   1 + c.branch + (c.gate == LSH_GATE_SIGMOID),
+                                   c.branch ? 4 : 2, c.branch ? kFwdCtas : kFwdNormCtas});
   const SubArgs a = sub_args(c, s);
   return c.dtype == LSH_BF16 ? sub_fwd_type<__nv_bfloat16>(c, a, s, st)
                              : sub_fwd_type<float>(c, a, s, st);
@@ -142,20 +157,28 @@ __global__ void __launch_bounds__(1024) sub_final_kernel(const FinalArgs a) {
   }
 }
 
+template <class T>
+SubShape bwd_shape(const SubCall& c, int tensors) {
+  using Z = BwdSize<T>;
+  return sub_shape(c, {kBwdPer, Z::kTok, Z::kThreads, tensors,
+                       (c.norm != LSH_NORM_NONE) + 2 * c.branch, Z::kCtas});
+}
+
 }  // namespace
 
 size_t sub_bwd_ws_bytes(int B, int H, int L, int d, bool branch, bool gate_batch) {
-  // as many rows as any kernel of the calls writes
+  // no call's kernel has more CTAs than this, whatever its layout
   const int D = H * d, groups = gate_batch ? B : 1;
   const int64_t tokens = gate_batch ? L : (int64_t)B * L;
-  const int64_t parts = std::min<int64_t>(tokens, std::max(1, kBwdParts / std::max(1, groups)));
+  const int64_t parts = std::min<int64_t>(tokens, max_parts(kMaxParts, groups));
   return align_up((size_t)groups * parts * (branch ? 4 : 2) * D * 4, 256);
 }
 
 cudaError_t launch_sub_bwd(const SubCall& c, void* ws, cudaStream_t st) {
   const bool norm = c.norm != LSH_NORM_NONE;
   const int tensors = 2 * norm + (c.dy != nullptr) + c.branch + (c.gate == LSH_GATE_SIGMOID);
-  const SubShape s = sub_shape(c, {kBwdPer, tensors, norm + 2 * c.branch, 2});
+  const SubShape s = c.dtype == LSH_BF16 ? bwd_shape<__nv_bfloat16>(c, tensors)
+                                         : bwd_shape<float>(c, tensors);
   SubArgs a = sub_args(c, s);
   const bool sums = c.dgate || c.dwp || c.dbp || c.dw || c.db;
   a.part = sums ? (float*)ws : nullptr;

@@ -35,7 +35,6 @@
 
 namespace lsh {
 
-constexpr int kTeamThreads = 256; // threads of a CTA of several teams
 constexpr int kMaxWarps = 16;     // of a team
 constexpr int kNarrowPer = 16;    // features a thread of the element-wise kernels
 constexpr int kMaxStages = 4;
@@ -162,10 +161,12 @@ __device__ __forceinline__ void cp_wait_for(int pending) {
 // (V = 8 or 4) go through the ring; V = 1 (odd sizes, unaligned arrays) loads
 // element by element.
 // Group g of a per-batch gate is batch g; otherwise the one group is all B L
-// tokens in order. A warp's teams take neighbouring tokens; `live` is false
-// where a team has run out of them and only goes along.
+// tokens in order. A team takes TOK neighbouring tokens at a time, so that
+// parameters, flags and addresses are read once for them, and a warp's teams
+// neighbouring ones; `live` is false for a token past the last, which a team
+// only goes along with.
 // TEAM: threads of a token up to a warp, or 0: whole warps, a.team threads.
-template <class T, int V, int PER, int TEAM, int NVEC>
+template <class T, int V, int PER, int TEAM, int NVEC, int TOK, int THREADS>
 struct Place {
   static constexpr bool kMulti = TEAM == 0;
   static constexpr int NV = PER / V;
@@ -199,15 +200,15 @@ struct Place {
     }
     par = (uint32_t)__cvta_generic_to_shared(smem) + lane * 16;
     unsigned char* p = smem + NVEC * (PER / 4) * team() * 16;
-    red = reinterpret_cast<float*>(p) + team_id * (8 * kMaxWarps);
-    if (kMulti) p += a.teams * (32 * kMaxWarps);
+    red = reinterpret_cast<float*>(p) + team_id * (16 * kMaxWarps);
+    if (kMulti) p += a.teams * (64 * kMaxWarps);
     ring = (uint32_t)__cvta_generic_to_shared(p) + threadIdx.x * 16;
   }
-  // bytes from a slot to the next, from a tensor to the next
+  // bytes from a slot to the next, from a token's vectors of a tensor to the next
   __device__ __forceinline__ uint32_t slot() const {
-    return kMulti ? blockDim.x * 16 : kTeamThreads * 16;
+    return kMulti ? blockDim.x * 16 : THREADS * 16;
   }
-  __device__ __forceinline__ uint32_t tensor() const { return kSlots * slot(); }
+  __device__ __forceinline__ uint32_t one() const { return kSlots * slot(); }
   __device__ __forceinline__ int team() const { return kMulti ? a.team : TEAM; }
   __device__ __forceinline__ bool on(int k) const { return on_bits >> k & 1; }
   __device__ __forceinline__ int unit(int k) const { return on(k) ? lane + k * team() : 0; }
@@ -221,8 +222,8 @@ struct Place {
   }
 
   // ---- tokens ----
-  __device__ __forceinline__ int first() const { return part * a.teams + team_id; }
-  __device__ __forceinline__ int step() const { return a.parts * a.teams; }
+  __device__ __forceinline__ int first() const { return (part * a.teams + team_id) * TOK; }
+  __device__ __forceinline__ int step() const { return a.parts * a.teams * TOK; }
   // Rounds that every team of a warp (of a CTA where one is the team) makes,
   // uniform over the warp.
   __device__ __forceinline__ int rounds() const {
@@ -242,35 +243,34 @@ struct Place {
     return b * s.b + l * s.l;
   }
 
-  // Sums of N values over the team, the same on each of its threads. Two or
-  // four values share one butterfly: the first one or two exchanges split the
-  // values between the halves (quarters) of the team instead of adding the
-  // same sums on both, 14 and 22 instructions a warp instead of 20 and 40.
-  // `red` holds two buffers used in turn, so one barrier a call is enough.
+  // Sums of N values over the team, the same on each of its threads. Several
+  // values share one butterfly: the first exchanges split the values between
+  // the halves of the team instead of adding the same sums on both (for 2, 4,
+  // 8 values 14, 22, 40 instructions a warp instead of 20, 40, 80). `red`
+  // holds two buffers used in turn, so one barrier a call is enough.
   template <int N>
   __device__ __forceinline__ void team_sum(float (&v)[N]) {
     constexpr int W = kMulti ? 32 : TEAM;
+    constexpr int S = N < W / 2 ? N : 1;   // values to split
     const unsigned all = 0xffffffffu;
     const int me = threadIdx.x & 31;
-    if constexpr (N == 4 && W >= 4) {
-      const bool up1 = me & (W / 2), up2 = me & (W / 4);
-      float x = up1 ? v[2] : v[0], y = up1 ? v[3] : v[1];
-      x += __shfl_xor_sync(all, up1 ? v[0] : v[2], W / 2);
-      y += __shfl_xor_sync(all, up1 ? v[1] : v[3], W / 2);
-      float z = up2 ? y : x;
-      z += __shfl_xor_sync(all, up2 ? x : y, W / 4);
+    if constexpr (S > 1) {
+      float x[N];
 #pragma unroll
-      for (int o = W / 8; o > 0; o >>= 1) z += __shfl_xor_sync(all, z, o);
+      for (int i = 0; i < N; ++i) x[i] = v[i];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(all, z, i * (W / 4), W);
-    } else if constexpr (N == 2 && W >= 8) {
-      const bool up1 = me & (W / 2);
-      float x = up1 ? v[1] : v[0];
-      x += __shfl_xor_sync(all, up1 ? v[0] : v[1], W / 2);
+      for (int n = N / 2, o = W / 2; n > 0; n /= 2, o /= 2) {
+        const bool upper = me & o;
 #pragma unroll
-      for (int o = W / 4; o > 0; o >>= 1) x += __shfl_xor_sync(all, x, o);
+        for (int i = 0; i < n; ++i) {
+          const float keep = upper ? x[i + n] : x[i], send = upper ? x[i] : x[i + n];
+          x[i] = keep + __shfl_xor_sync(all, send, o);
+        }
+      }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) v[i] = __shfl_sync(all, x, i * (W / 2), W);
+      for (int o = W / N / 2; o > 0; o >>= 1) x[0] += __shfl_xor_sync(all, x[0], o);
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = __shfl_sync(all, x[0], i * (W / N), W);
     } else {
 #pragma unroll
       for (int o = W / 2; o > 0; o >>= 1)
@@ -278,7 +278,7 @@ struct Place {
         for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(all, v[i], o);
     }
     if constexpr (kMulti) {
-      float* r = red + turn * (4 * kMaxWarps);
+      float* r = red + turn * (8 * kMaxWarps);
       turn ^= 1;
       const int nw = a.team >> 5;
       if ((lane & 31) == 0) {
@@ -417,22 +417,30 @@ struct Place {
     lo = pk(__uint_as_float(u.x), __uint_as_float(u.y));
     hi = pk(__uint_as_float(u.z), __uint_as_float(u.w));
   }
-  __device__ __forceinline__ void scale_by(int vec, f2 (&v)[P]) const {
+  template <int N>
+  __device__ __forceinline__ void scale_by(int vec, f2 (&v)[N][P]) const {
 #pragma unroll
     for (int j = 0; j < PER / 4; ++j) {
       f2 lo, hi;
       params(vec, j, lo, hi);
-      v[2 * j] = mul2(v[2 * j], lo);
-      v[2 * j + 1] = mul2(v[2 * j + 1], hi);
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        v[n][2 * j] = mul2(v[n][2 * j], lo);
+        v[n][2 * j + 1] = mul2(v[n][2 * j + 1], hi);
+      }
     }
   }
-  __device__ __forceinline__ void shift_by(int vec, f2 (&v)[P]) const {
+  template <int N>
+  __device__ __forceinline__ void shift_by(int vec, f2 (&v)[N][P]) const {
 #pragma unroll
     for (int j = 0; j < PER / 4; ++j) {
       f2 lo, hi;
       params(vec, j, lo, hi);
-      v[2 * j] = add2(v[2 * j], lo);
-      v[2 * j + 1] = add2(v[2 * j + 1], hi);
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        v[n][2 * j] = add2(v[n][2 * j], lo);
+        v[n][2 * j + 1] = add2(v[n][2 * j + 1], hi);
+      }
     }
   }
 
@@ -491,11 +499,11 @@ __device__ __forceinline__ float inv_std(float sum_sq, float inv_d, float eps) {
 // one stage has to fit, and a token's vectors have to lie within 2^31 elements
 // of its first.
 struct SubShape {
-  int team, teams, threads, groups, tokens, parts, stages, smem;
+  int team, teams, threads, tok, groups, tokens, parts, stages, smem;
   bool wide;
 };
 struct SubSize {
-  int per, tensors, vecs, ctas;   // of the wide kernel
+  int per, tok, threads, tensors, vecs, ctas;   // of the wide kernel
 };
 SubShape sub_shape(const SubCall& c, const SubSize& z);
 SubArgs sub_args(const SubCall& c, const SubShape& s);
@@ -514,14 +522,27 @@ cudaError_t with_team(int team, F f) {
   }
 }
 
-constexpr int kFwdPer = 32, kBwdPer = 16;   // features a thread of the wide kernels
+// Features a thread, tokens a team, threads of a CTA of several teams and CTAs
+// of an SM, for the wide kernels. Forward: 32 features, so that a warp takes
+// two tokens of 512. Backward: the four sums of parameter gradients already
+// take four registers a feature, so 16 features, and two tokens at a time in
+// bf16; in float32, where a token is twice the bytes, one.
+constexpr int kFwdPer = 32, kFwdThreads = 256, kFwdCtas = 2, kFwdNormCtas = 3;
+constexpr int kBwdPer = 16;
+constexpr int kNarrowThreads = 256;
+template <class T>
+struct BwdSize {
+  static constexpr int kTok = sizeof(T) == 2 ? 2 : 1;
+  static constexpr int kThreads = sizeof(T) == 2 ? 128 : 256;
+  static constexpr int kCtas = sizeof(T) == 2 ? 3 : 2;
+};
 
 template <class T>
 cudaError_t sub_fwd_type(const SubCall& c, const SubArgs& a, const SubShape& s, cudaStream_t st);
 template <class T, bool NORM>
 cudaError_t sub_bwd_type(const SubCall& c, const SubArgs& a, const SubShape& s, cudaStream_t st);
 
-// Rows of partial sums a backward call may write (of any kernel).
-constexpr int kBwdParts = 2 * kSms;
+// CTAs of a call, and so rows of partial sums of a backward one, at most.
+constexpr int kMaxParts = 4 * kSms;
 
 }  // namespace lsh

@@ -47,11 +47,15 @@ __device__ __forceinline__ void write_part(const At& at, const f2 (&s)[At::P], f
 
 // Parameters, in order: W, P1 = gate w_post (a sigmoid gate is not in it), P0
 // = b_post (sigmoid gates only).
-template <class T, int V, int PER, int TEAM, bool BRANCH, bool NORM, bool POST, bool SIG>
-__global__ void __launch_bounds__(TEAM == 0 ? 32 * kMaxWarps : kTeamThreads, TEAM == 0 ? 1 : 2)
+template <class T, int V, int PER, int TEAM, int TOK, bool BRANCH, bool NORM, bool POST, bool SIG>
+__global__ void __launch_bounds__(TEAM != 0  ? (V == 1 ? kNarrowThreads : BwdSize<T>::kThreads)
+                                  : TOK == 1 ? 32 * kMaxWarps
+                                             : 256,
+                                  TEAM != 0 ? (V == 1 ? 2 : BwdSize<T>::kCtas) : 1)
 sub_bwd_kernel(const __grid_constant__ SubArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
-  using At = Place<T, V, PER, TEAM, (NORM ? 1 : 0) + (BRANCH ? 2 : 0)>;
+  using At = Place<T, V, PER, TEAM, (NORM ? 1 : 0) + (BRANCH ? 2 : 0), TOK,
+                   V == 1 ? kNarrowThreads : BwdSize<T>::kThreads>;
   constexpr int P = At::P;
   constexpr int kP1 = NORM ? 1 : 0, kP0 = kP1 + 1;
   At at(a, smem);
@@ -64,12 +68,12 @@ sub_bwd_kernel(const __grid_constant__ SubArgs a) {
   // the ring's tensors: y dh, dy, f, z
   const int i_dy = NORM ? 2 : 0, i_f = i_dy + (a.dy ? 1 : 0), i_z = i_f + 1;
   const int tensors = i_f + BRANCH + sig;
-  at.clear(at.ring, a.stages * tensors);
+  at.clear(at.ring, a.stages * tensors * TOK);
   __syncthreads();
   const uint64_t offset = a.offset + (a.counter ? __ldg(a.counter) : 0);
   const int step = at.step(), rounds = at.rounds();
-  const uint32_t one = at.tensor();
-  const uint32_t stage_bytes = tensors * one;
+  const uint32_t one = at.one(), token_bytes = tensors * one, stage_bytes = TOK * token_bytes;
+  const bool lf = post && a.post == LSH_NORM_LAYER, ly = NORM && a.norm == LSH_NORM_LAYER;
   f2 sa[P], sb[P], s1[P], s0[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) sa[i] = sb[i] = s1[i] = s0[i] = 0ull;
@@ -79,23 +83,27 @@ sub_bwd_kernel(const __grid_constant__ SubArgs a) {
   auto copy = [&]() {
     if constexpr (At::kRing) {
       if (n_in < rounds) {
-        if (t_in < a.tokens) {
-          int b, l;
-          at.token(t_in, b, l);
-          const int64_t rx = At::row(a.sx, b, l);
-          if constexpr (NORM) {
-            at.issue(a.x, at.ox, rx, s_in);
-            at.issue(a.dh, BRANCH ? at.ox : at.oh, BRANCH ? rx : At::row(a.sh, b, l), s_in + one);
+#pragma unroll
+        for (int j = 0; j < TOK; ++j) {
+          const uint32_t to = s_in + j * token_bytes;
+          if (t_in + j < a.tokens) {
+            int b, l;
+            at.token(t_in + j, b, l);
+            const int64_t rx = At::row(a.sx, b, l);
+            if constexpr (NORM) {
+              at.issue(a.x, at.ox, rx, to);
+              at.issue(a.dh, BRANCH ? at.ox : at.oh, BRANCH ? rx : At::row(a.sh, b, l), to + one);
+            }
+            if (a.dy) at.issue(a.dy, at.ox, rx, to + i_dy * one);
+            if constexpr (BRANCH) {
+              const int64_t rf = At::row(a.sf, b, l);
+              at.issue(a.f, at.of, rf, to + i_f * one);
+              if (sig) at.issue(a.z, at.of, rf, to + i_z * one);
+            }
+          } else {
+            // nothing may be added for a token that is not there
+            at.clear(to, tensors);
           }
-          if (a.dy) at.issue(a.dy, at.ox, rx, s_in + i_dy * one);
-          if constexpr (BRANCH) {
-            const int64_t rf = At::row(a.sf, b, l);
-            at.issue(a.f, at.of, rf, s_in + i_f * one);
-            if (sig) at.issue(a.z, at.of, rf, s_in + i_z * one);
-          }
-        } else {
-          // nothing may be added for a token that is not there
-          at.clear(s_in, tensors);
         }
         t_in += step;
         ++n_in;
@@ -111,123 +119,182 @@ sub_bwd_kernel(const __grid_constant__ SubArgs a) {
   for (int n = 0; n < rounds; ++n, t += step) {
     copy();
     if constexpr (At::kRing) cp_wait_for(a.stages - 1);
-    const bool live = At::kMulti || t < a.tokens;
-    int b, l;
-    at.token(t, b, l);
-    f2 q[P];     // T, then q, then du
-    f2 hat[P];   // y - mean, then f - mean, then fhat
-    float r_f = 0.f, mean_f = 0.f;
+    int b[TOK], l[TOK];
+    bool live[TOK];
+#pragma unroll
+    for (int j = 0; j < TOK; ++j) {
+      live[j] = (At::kMulti && TOK == 1) || t + j < a.tokens;
+      at.token(t + j, b[j], l[j]);
+    }
+    auto get_x = [&](const void* p, int i, int j, f2(&v)[P]) {
+      at.get(p, a.sx, b[j], l[j], live[j], st + j * token_bytes + i * one, v);
+    };
+    auto get_f = [&](const void* p, int i, int j, f2(&v)[P]) {
+      at.get(p, a.sf, b[j], l[j], live[j], st + j * token_bytes + i * one, v);
+    };
+    auto get_dh = [&](int j, f2(&v)[P]) {
+      at.get(a.dh, a.sh, b[j], l[j], live[j], st + j * token_bytes + one, v);
+    };
+    f2 q[TOK][P];     // T, then q, then du
+    f2 hat[TOK][P];   // y - mean, then f - mean, then fhat
+    float r_f[TOK], mean_f[TOK];
     if constexpr (NORM) {
-      at.get(a.x, a.sx, b, l, live, st, hat);
-      const bool lf = post && a.post == LSH_NORM_LAYER, ly = a.norm == LSH_NORM_LAYER;
+#pragma unroll
+      for (int j = 0; j < TOK; ++j) {
+        get_x(a.x, 0, j, hat[j]);
+        mean_f[j] = 0.f;
+      }
       if (lf || ly) {
-        float s[2] = {0.f, 0.f};
-        if (ly) s[0] = sum_all(hat);
-        if (lf) {
-          f2 f[P];
-          at.get(a.f, a.sf, b, l, live, st + i_f * one, f);
-          s[1] = sum_all(f);
+        float s[2 * TOK];
+#pragma unroll
+        for (int j = 0; j < TOK; ++j) {
+          s[2 * j] = sum_all(hat[j]);
+          s[2 * j + 1] = 0.f;
+          if (lf) {
+            get_f(a.f, i_f, j, q[j]);
+            s[2 * j + 1] = sum_all(q[j]);
+          }
         }
         at.team_sum(s);
-        if (ly) at.center(hat, s[0] * a.inv_d);
-        mean_f = s[1] * a.inv_d;
-      }
-      float s[4];
-      s[3] = 0.f;
-      if (post) {
-        f2 f[P];
-        at.get(a.f, a.sf, b, l, live, st + i_f * one, f);
-        if (lf) at.center(f, mean_f);
-        s[3] = dot_all(f, f);
-      }
-      s[0] = dot_all(hat, hat);
-      at.get(a.dh, a.sh, b, l, live, st + one, q);
 #pragma unroll
-      for (int i = 0; i < P; ++i) sb[i] = add2(sb[i], q[i]);
+        for (int j = 0; j < TOK; ++j) {
+          if (ly) at.center(hat[j], s[2 * j] * a.inv_d);
+          mean_f[j] = s[2 * j + 1] * a.inv_d;
+        }
+      }
+      float s[4 * TOK];
+#pragma unroll
+      for (int j = 0; j < TOK; ++j) {
+        s[4 * j + 3] = 0.f;
+        if (post) {
+          get_f(a.f, i_f, j, q[j]);
+          if (lf) at.center(q[j], mean_f[j]);
+          s[4 * j + 3] = dot_all(q[j], q[j]);
+        }
+        s[4 * j] = dot_all(hat[j], hat[j]);
+        get_dh(j, q[j]);
+#pragma unroll
+        for (int i = 0; i < P; ++i) sb[i] = add2(sb[i], q[j][i]);
+      }
       at.scale_by(0, q);
-      s[1] = sum_all(q);
-      s[2] = dot_all(q, hat);
-      at.team_sum(s);
-      const float r = inv_std(s[0], a.inv_d, a.eps);
-      if (post) r_f = inv_std(s[3], a.inv_d, a.eps_post);
-      const float m0 = ly ? s[1] * a.inv_d : 0.f, m1 = r * r * s[2] * a.inv_d;
-      const f2 r2 = pk(r, r), k0 = pk(-r * m0, -r * m0), k1 = pk(-r * m1, -r * m1);
-      {
-        f2 dh[P];
-        at.get(a.dh, a.sh, b, l, live, st + one, dh);
 #pragma unroll
-        for (int i = 0; i < P; ++i) sa[i] = fma2(dh[i], mul2(hat[i], r2), sa[i]);
+      for (int j = 0; j < TOK; ++j) {
+        s[4 * j + 1] = sum_all(q[j]);
+        s[4 * j + 2] = dot_all(q[j], hat[j]);
       }
+      at.team_sum(s);
 #pragma unroll
-      for (int i = 0; i < P; ++i) q[i] = fma2(q[i], r2, fma2(hat[i], k1, k0));
+      for (int j = 0; j < TOK; ++j) {
+        const float r = inv_std(s[4 * j], a.inv_d, a.eps);
+        if (post) r_f[j] = inv_std(s[4 * j + 3], a.inv_d, a.eps_post);
+        const float m0 = ly ? s[4 * j + 1] * a.inv_d : 0.f, m1 = r * r * s[4 * j + 2] * a.inv_d;
+        const f2 r2 = pk(r, r), k0 = pk(-r * m0, -r * m0), k1 = pk(-r * m1, -r * m1);
+        {
+          f2 dh[P];
+          get_dh(j, dh);
+#pragma unroll
+          for (int i = 0; i < P; ++i) sa[i] = fma2(dh[i], mul2(hat[j][i], r2), sa[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < P; ++i) q[j][i] = fma2(q[j][i], r2, fma2(hat[j][i], k1, k0));
+      }
       if (a.dy) {
-        f2 dy[P];
-        at.get(a.dy, a.sx, b, l, live, st + i_dy * one, dy);
 #pragma unroll
-        for (int i = 0; i < P; ++i) q[i] = add2(q[i], dy[i]);
+        for (int j = 0; j < TOK; ++j) {
+          get_x(a.dy, i_dy, j, hat[j]);
+#pragma unroll
+          for (int i = 0; i < P; ++i) q[j][i] = add2(q[j][i], hat[j][i]);
+        }
       }
     } else {
-      at.get(a.dy, a.sx, b, l, live, st + i_dy * one, q);
+#pragma unroll
+      for (int j = 0; j < TOK; ++j) get_x(a.dy, i_dy, j, q[j]);
     }
     if (a.dx) {
-      f2 o[P];
 #pragma unroll
-      for (int i = 0; i < P; ++i) o[i] = q[i];
-      if (BRANCH && a.beta != 1.f) scale_all(o, a.beta);
-      at.template put<false>(a.dx, a.sx, at.ox, b, l, live, o);
+      for (int j = 0; j < TOK; ++j) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) hat[j][i] = BRANCH ? mul2(q[j][i], pk(a.beta, a.beta)) : q[j][i];
+        at.template put<false>(a.dx, a.sx, at.ox, b[j], l[j], live[j], hat[j]);
+      }
     }
     if constexpr (BRANCH) {
-      at.get(a.f, a.sf, b, l, live, st + i_f * one, hat);
-      if (post) {
-        if constexpr (NORM) {
-          if (a.post == LSH_NORM_LAYER) at.center(hat, mean_f);
-        } else {
-          float s[1];
-          if (a.post == LSH_NORM_LAYER) {
-            s[0] = sum_all(hat);
-            at.team_sum(s);
-            at.center(hat, s[0] * a.inv_d);
-          }
-          s[0] = dot_all(hat, hat);
-          at.team_sum(s);
-          r_f = inv_std(s[0], a.inv_d, a.eps_post);
-        }
-        scale_all(hat, r_f);
-      }
-      if (a.drop_t) at.drop_all(offset, b, l, a.alpha * a.drop_scale, q);
-      else scale_all(q, a.alpha);
-      if (sig) {
-        f2 u[P], z[P];
 #pragma unroll
-        for (int i = 0; i < P; ++i) u[i] = hat[i];
-        if (post && a.wp) at.scale_by(kP1, u);
-        if (has0) at.shift_by(kP0, u);
-        at.get(a.z, a.sf, b, l, live, st + i_z * one, z);
+      for (int j = 0; j < TOK; ++j) get_f(a.f, i_f, j, hat[j]);
+      if (post) {
+        if constexpr (!NORM) {
+          float s[TOK];
+          if (lf) {
+#pragma unroll
+            for (int j = 0; j < TOK; ++j) s[j] = sum_all(hat[j]);
+            at.team_sum(s);
+#pragma unroll
+            for (int j = 0; j < TOK; ++j) at.center(hat[j], s[j] * a.inv_d);
+          }
+#pragma unroll
+          for (int j = 0; j < TOK; ++j) s[j] = dot_all(hat[j], hat[j]);
+          at.team_sum(s);
+#pragma unroll
+          for (int j = 0; j < TOK; ++j) r_f[j] = inv_std(s[j], a.inv_d, a.eps_post);
+        } else if (lf) {
+#pragma unroll
+          for (int j = 0; j < TOK; ++j) at.center(hat[j], mean_f[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < TOK; ++j) scale_all(hat[j], r_f[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < TOK; ++j) {
+        if (a.drop_t) at.drop_all(offset, b[j], l[j], a.alpha * a.drop_scale, q[j]);
+        else scale_all(q[j], a.alpha);
+      }
+      if constexpr (sig) {
+#pragma unroll
+        for (int j = 0; j < TOK; ++j) {
+          f2 u[1][P], z[P];
+#pragma unroll
+          for (int i = 0; i < P; ++i) u[0][i] = hat[j][i];
+          if (post && a.wp) at.scale_by(kP1, u);
+          if (has0) at.shift_by(kP0, u);
+          get_f(a.z, i_z, j, z);
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            const float2 w = up(z[i]);
+            float d0, d1;
+            const float g0 = sigmoid(w.x, d0), g1 = sigmoid(w.y, d1);
+            u[0][i] = mul2(u[0][i], mul2(q[j][i], pk(d0, d1)));
+            q[j][i] = mul2(q[j][i], pk(g0, g1));
+          }
+          if (a.dz) at.template put<false>(a.dz, a.sf, at.of, b[j], l[j], live[j], u[0]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < TOK; ++j)
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-          const float2 w = up(z[i]);
-          float d0, d1;
-          const float g0 = sigmoid(w.x, d0), g1 = sigmoid(w.y, d1);
-          u[i] = mul2(u[i], mul2(q[i], pk(d0, d1)));
-          q[i] = mul2(q[i], pk(g0, g1));
+          s1[i] = fma2(q[j][i], hat[j][i], s1[i]);
+          s0[i] = add2(s0[i], q[j][i]);
         }
-        if (a.dz) at.template put<false>(a.dz, a.sf, at.of, b, l, live, u);
-      }
-#pragma unroll
-      for (int i = 0; i < P; ++i) {
-        s1[i] = fma2(q[i], hat[i], s1[i]);
-        s0[i] = add2(s0[i], q[i]);
-      }
       if (has1) at.scale_by(kP1, q);
       if (post) {
-        float s[2] = {sum_all(q), dot_all(q, hat)};
-        at.team_sum(s);
-        const float m0 = a.post == LSH_NORM_LAYER ? s[0] * a.inv_d : 0.f, m1 = s[1] * a.inv_d;
-        const f2 r2 = pk(r_f, r_f), k0 = pk(-r_f * m0, -r_f * m0), k1 = pk(-r_f * m1, -r_f * m1);
+        float s[2 * TOK];
 #pragma unroll
-        for (int i = 0; i < P; ++i) q[i] = fma2(q[i], r2, fma2(hat[i], k1, k0));
+        for (int j = 0; j < TOK; ++j) {
+          s[2 * j] = sum_all(q[j]);
+          s[2 * j + 1] = dot_all(q[j], hat[j]);
+        }
+        at.team_sum(s);
+#pragma unroll
+        for (int j = 0; j < TOK; ++j) {
+          const float r = r_f[j], m0 = lf ? s[2 * j] * a.inv_d : 0.f, m1 = s[2 * j + 1] * a.inv_d;
+          const f2 r2 = pk(r, r), k0 = pk(-r * m0, -r * m0), k1 = pk(-r * m1, -r * m1);
+#pragma unroll
+          for (int i = 0; i < P; ++i) q[j][i] = fma2(q[j][i], r2, fma2(hat[j][i], k1, k0));
+        }
       }
-      at.template put<false>(a.df, a.sf, at.of, b, l, live, q);
+#pragma unroll
+      for (int j = 0; j < TOK; ++j)
+        at.template put<false>(a.df, a.sf, at.of, b[j], l[j], live[j], q[j]);
     }
     st += stage_bytes;
     if (st == at.ring + a.stages * stage_bytes) st = at.ring;
@@ -249,15 +316,15 @@ sub_bwd_kernel(const __grid_constant__ SubArgs a) {
   }
 }
 
-template <class T, int V, int PER, int TEAM, bool NORM>
+template <class T, int V, int PER, int TEAM, int TOK, bool NORM>
 cudaError_t run_branch(const SubCall& c, const SubArgs& a, const SubShape& s, cudaStream_t st) {
   const bool sig = c.gate == LSH_GATE_SIGMOID, post = c.post != LSH_NORM_NONE;
-  auto fn = post && sig ? sub_bwd_kernel<T, V, PER, TEAM, true, NORM, true, true>
-            : post      ? sub_bwd_kernel<T, V, PER, TEAM, true, NORM, true, false>
-            : sig       ? sub_bwd_kernel<T, V, PER, TEAM, true, NORM, false, true>
-                        : sub_bwd_kernel<T, V, PER, TEAM, true, NORM, false, false>;
+  auto fn = post && sig ? sub_bwd_kernel<T, V, PER, TEAM, TOK, true, NORM, true, true>
+            : post      ? sub_bwd_kernel<T, V, PER, TEAM, TOK, true, NORM, true, false>
+            : sig       ? sub_bwd_kernel<T, V, PER, TEAM, TOK, true, NORM, false, true>
+                        : sub_bwd_kernel<T, V, PER, TEAM, TOK, true, NORM, false, false>;
   if constexpr (NORM)
-    if (!c.branch) fn = sub_bwd_kernel<T, V, PER, TEAM, false, true, false, false>;
+    if (!c.branch) fn = sub_bwd_kernel<T, V, PER, TEAM, TOK, false, true, false, false>;
   // the row of partial sums goes through the same memory
   const int smem = std::max(s.smem, s.teams * a.D * 4);
   if (smem > kSmemDefault) {
@@ -274,12 +341,14 @@ cudaError_t run_branch(const SubCall& c, const SubArgs& a, const SubShape& s, cu
 
 template <class T, bool NORM>
 cudaError_t sub_bwd_type(const SubCall& c, const SubArgs& a, const SubShape& s, cudaStream_t st) {
+  constexpr int V = 16 / (int)sizeof(T), TOK = BwdSize<T>::kTok;
+  if (s.wide && s.tok < TOK) return run_branch<T, V, kBwdPer, 0, 1, NORM>(c, a, s, st);
   if (s.wide)
     return with_team(s.team, [&](auto t) {
-      return run_branch<T, 16 / (int)sizeof(T), kBwdPer, t.value, NORM>(c, a, s, st);
+      return run_branch<T, V, kBwdPer, t.value, TOK, NORM>(c, a, s, st);
     });
-  return s.team == 32 ? run_branch<T, 1, kNarrowPer, 32, NORM>(c, a, s, st)
-                      : run_branch<T, 1, kNarrowPer, 0, NORM>(c, a, s, st);
+  return s.team == 32 ? run_branch<T, 1, kNarrowPer, 32, 1, NORM>(c, a, s, st)
+                      : run_branch<T, 1, kNarrowPer, 0, 1, NORM>(c, a, s, st);
 }
 
 }  // namespace lsh

@@ -10,10 +10,13 @@ namespace {
 // Parameters, in order: P1 = gate w_post, P0 = gate b_post (a sigmoid gate is
 // not in them), W, B: the products are formed once a CTA, not once a token.
 template <class T, int V, int PER, int TEAM, bool BRANCH, bool POST, bool SIG>
-__global__ void __launch_bounds__(V == 1 ? 32 * kMaxWarps : kTeamThreads)
+__global__ void __launch_bounds__(V == 1 ? 32 * kMaxWarps : kFwdThreads,
+                                  V == 1   ? 1
+                                  : BRANCH ? kFwdCtas
+                                           : kFwdNormCtas)
 sub_fwd_kernel(const __grid_constant__ SubArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
-  using At = Place<T, V, PER, TEAM, BRANCH ? 4 : 2>;
+  using At = Place<T, V, PER, TEAM, BRANCH ? 4 : 2, 1, V == 1 ? kNarrowThreads : kFwdThreads>;
   constexpr int P = At::P;
   At at(a, smem);
   constexpr bool post = BRANCH && POST, sig = BRANCH && SIG;
@@ -30,7 +33,7 @@ sub_fwd_kernel(const __grid_constant__ SubArgs a) {
   __syncthreads();
   const uint64_t offset = a.offset + (a.counter ? __ldg(a.counter) : 0);
   const int step = at.step(), rounds = at.rounds();
-  const uint32_t stage_bytes = tensors * at.tensor();
+  const uint32_t stage_bytes = tensors * at.one();
 
   int t_in = at.first(), n_in = 0;
   uint32_t s_in = at.ring;      // where the next token's copies go
@@ -44,8 +47,8 @@ sub_fwd_kernel(const __grid_constant__ SubArgs a) {
           at.issue(a.x, at.ox, rx, s_in);
           if constexpr (BRANCH) {
             const int64_t rf = At::row(a.sf, b, l);
-            at.issue(a.f, at.of, rf, s_in + at.tensor());
-            if (sig) at.issue(a.z, at.of, rf, s_in + 2 * at.tensor());
+            at.issue(a.f, at.of, rf, s_in + at.one());
+            if (sig) at.issue(a.z, at.of, rf, s_in + 2 * at.one());
           }
         }
         t_in += step;
@@ -65,9 +68,10 @@ sub_fwd_kernel(const __grid_constant__ SubArgs a) {
     const bool live = At::kMulti || t < a.tokens;
     int b, l;
     at.token(t, b, l);
-    f2 v[P];
+    f2 row[1][P];
+    f2(&v)[P] = row[0];
     if constexpr (BRANCH) {
-      at.get(a.f, a.sf, b, l, live, st + at.tensor(), v);
+      at.get(a.f, a.sf, b, l, live, st + at.one(), v);
       if (post) {
         float s[1];
         if (a.post == LSH_NORM_LAYER) {
@@ -79,11 +83,11 @@ sub_fwd_kernel(const __grid_constant__ SubArgs a) {
         at.team_sum(s);
         scale_all(v, inv_std(s[0], a.inv_d, a.eps_post));
       }
-      if (has1) at.scale_by(0, v);
-      if (has0) at.shift_by(1, v);
+      if (has1) at.scale_by(0, row);
+      if (has0) at.shift_by(1, row);
       if (sig) {
         f2 z[P];
-        at.get(a.z, a.sf, b, l, live, st + 2 * at.tensor(), z);
+        at.get(a.z, a.sf, b, l, live, st + 2 * at.one(), z);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
           const float2 u = up(z[i]);
@@ -118,8 +122,8 @@ sub_fwd_kernel(const __grid_constant__ SubArgs a) {
       s[0] = dot_all(v, v);
       at.team_sum(s);
       scale_all(v, inv_std(s[0], a.inv_d, a.eps));
-      if (a.w) at.scale_by(kW, v);
-      if (a.b) at.shift_by(kB, v);
+      if (a.w) at.scale_by(kW, row);
+      if (a.b) at.shift_by(kB, row);
       at.template put<false>(a.h, a.sh, BRANCH ? at.ox : at.oh, b, l, live, v);
     }
     st += stage_bytes;

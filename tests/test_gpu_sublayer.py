@@ -511,3 +511,44 @@ def test_two_drivers_at_once_on_two_streams():
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+@pytest.mark.parametrize("H,d,dtype,tokens", [
+    (1, 64, "bf16", 20000), (8, 64, "bf16", 20000), (16, 64, "bf16", 20000), (24, 64, "bf16", 9000),
+    (32, 64, "f32", 9000), (64, 64, "bf16", 9000), (100, 64, "bf16", 3000), (8, 63, "bf16", 9000),
+    (33, 31, "f32", 9000)])
+def test_backward_stays_inside_its_workspace(H, d, dtype, tokens):
+    """The partial sums of more tokens than the GPU holds at once: nothing
+    behind the workspace that the size query asks for is written."""
+    from efficient_transformer_lsh_b200 import _lib
+    torch = _torch()
+    td = torch.bfloat16 if dtype == "bf16" else torch.float32
+    B, L, D = 1, tokens, H * d
+    x, f, dy, dh, dx, df = (torch.randn(B, H, L, d, device="cuda").to(td) for _ in range(6))
+    w = torch.ones(D, device="cuda")
+    grads = [torch.empty(D, device="cuda") for _ in range(5)]
+    guard = 1 << 20
+
+    def room(n):
+        buf = torch.full((n + guard,), 77, dtype=torch.uint8, device="cuda")
+        return buf, n
+
+    n = _lib.make_norm_problem(B, H, L, d, dtype, _lib.LSH_NORM_LAYER, 1e-5)
+    buf, size = room(_lib.lsh_norm_bwd_workspace_size(n))
+    _lib.lsh_norm_bwd(n, x, w, dh, dy, dx, grads[0], grads[1], buf, size)
+    assert (buf[size:] == 77).all()
+    for norm in (_lib.LSH_NORM_NONE, _lib.LSH_NORM_RMS):
+        q = _lib.make_residual_problem(B, H, L, d, dtype, _lib.LSH_NORM_LAYER, norm,
+                                       _lib.LSH_GATE_VECTOR, False, 1e-5, 1e-5, 1.0, 1.0, 0.1)
+        buf, size = room(_lib.lsh_residual_bwd_workspace_size(q))
+        dw = grads[4] if norm else None
+        _lib.lsh_residual_bwd(q, dy, dh, x, f, w, w, w, w, 1, 0, None, dx, df, grads[0], grads[1],
+                              grads[2], dw, None, buf, size)
+        assert (buf[size:] == 77).all()
+    q = _lib.make_residual_problem(3, H, L // 3, d, dtype, _lib.LSH_NORM_LAYER, _lib.LSH_NORM_RMS,
+                                   _lib.LSH_GATE_VECTOR, True, 1e-5, 1e-5, 1.0, 1.0, 0.1)
+    buf, size = room(_lib.lsh_residual_bwd_workspace_size(q))
+    gate = torch.ones(3, D, device="cuda")
+    _lib.lsh_residual_bwd(q, dy, dh, x, f, gate, w, w, w, 1, 0, None, dx, df,
+                          torch.empty_like(gate), grads[1], grads[2], grads[4], None, buf, size)
+    assert (buf[size:] == 77).all()
