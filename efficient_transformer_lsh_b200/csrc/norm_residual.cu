@@ -111,6 +111,8 @@ struct FinalArgs {
 // then warp 0 adds the warps' sums.
 __global__ void __launch_bounds__(1024) sub_final_kernel(const FinalArgs a) {
   __shared__ float buf[2][32][33];
+  stream_wait();
+  let_next_start();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   const bool on = c < a.D;
@@ -120,10 +122,12 @@ __global__ void __launch_bounds__(1024) sub_final_kernel(const FinalArgs a) {
   for (int g = 0; g < a.groups; ++g) {
     float s1 = 0.f, s0 = 0.f;
     if (on) {
+      const float* r = a.part + ((int64_t)g * a.parts * a.vecs + v0) * a.D + c;
+      const int64_t row = (int64_t)a.vecs * a.D;
+#pragma unroll 8
       for (int p = w; p < a.parts; p += 32) {
-        const float* r = a.part + ((int64_t)(g * (int64_t)a.parts + p) * a.vecs + v0) * a.D + c;
-        s1 += __ldg(r);
-        s0 += __ldg(r + a.D);
+        s1 += __ldcg(r + p * row);
+        s0 += __ldcg(r + p * row + a.D);
       }
     }
     buf[0][w][lane] = s1;
@@ -199,10 +203,10 @@ cudaError_t launch_sub_bwd(const SubCall& c, void* ws, cudaStream_t st) {
   f.vecs = 2 * (f.norm + f.branch);
   f.wp = c.wp, f.bp = c.bp, f.gv = a.gv, f.gate_batch = c.gate_batch;
   f.dgate = c.dgate, f.dwp = c.dwp, f.dbp = c.dbp, f.dw = c.dw, f.db = c.db;
-  sub_final_kernel<<<dim3((unsigned)((a.D + 31) / 32), (unsigned)(f.norm + f.branch)), 1024, 0,
-                     st>>>(f);
   note_launch();
-  return cudaGetLastError();
+  return launch_overlapped(sub_final_kernel,
+                           dim3((unsigned)((a.D + 31) / 32), (unsigned)(f.norm + f.branch)), 1024,
+                           0, st, f);
 }
 
 }  // namespace lsh

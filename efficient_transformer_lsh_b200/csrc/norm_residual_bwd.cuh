@@ -59,6 +59,8 @@ sub_bwd_kernel(const __grid_constant__ SubArgs a) {
   constexpr int P = At::P;
   constexpr int kP1 = NORM ? 1 : 0, kP0 = kP1 + 1;
   At at(a, smem);
+  stream_wait();
+  let_next_start();
   constexpr bool post = BRANCH && POST, sig = BRANCH && SIG;
   const float* gv = a.gv ? a.gv + (int64_t)at.group * (a.gate_batch ? a.D : 0) : nullptr;
   const bool has1 = BRANCH && (a.wp || gv), has0 = sig && a.bp;
@@ -332,9 +334,8 @@ cudaError_t run_branch(const SubCall& c, const SubArgs& a, const SubShape& s, cu
         cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerSm);
     if (e != cudaSuccess) return e;
   }
-  fn<<<(unsigned)((int64_t)s.groups * s.parts), s.threads, smem, st>>>(a);
   note_launch();
-  return cudaGetLastError();
+  return launch_overlapped(fn, dim3((unsigned)((int64_t)s.groups * s.parts)), s.threads, smem, st, a);
 }
 
 }  // namespace

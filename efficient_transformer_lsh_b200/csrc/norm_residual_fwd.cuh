@@ -19,6 +19,8 @@ sub_fwd_kernel(const __grid_constant__ SubArgs a) {
   using At = Place<T, V, PER, TEAM, BRANCH ? 4 : 2, 1, V == 1 ? kNarrowThreads : kFwdThreads>;
   constexpr int P = At::P;
   At at(a, smem);
+  stream_wait();
+  let_next_start();
   constexpr bool post = BRANCH && POST, sig = BRANCH && SIG;
   const bool norm = a.norm != LSH_NORM_NONE;
   const float* gv = a.gv ? a.gv + (int64_t)at.group * (a.gate_batch ? a.D : 0) : nullptr;
@@ -145,9 +147,8 @@ cudaError_t run(const SubCall& c, const SubArgs& a, const SubShape& s, cudaStrea
         cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerSm);
     if (e != cudaSuccess) return e;
   }
-  fn<<<(unsigned)((int64_t)s.groups * s.parts), s.threads, s.smem, st>>>(a);
   note_launch();
-  return cudaGetLastError();
+  return launch_overlapped(fn, dim3((unsigned)((int64_t)s.groups * s.parts)), s.threads, s.smem, st, a);
 }
 
 }  // namespace

@@ -7,7 +7,10 @@
 // at position 2^20). Its top 32 bits, signed, are half turns in [-1, 1).
 //
 // Sine and cosine of a (token, pair) serve every head: a thread keeps those
-// of its pairs in registers and walks the heads.
+// of its pairs in registers and walks the heads, four rows in flight; with one
+// or two heads it takes four or two tokens instead. bf16 takes the hardware's
+// approximate sine and cosine (absolute error below 2^-21 on one turn, where
+// a bf16 result is rounded at 2^-9 of its value), float32 the accurate ones.
 #include <algorithm>
 
 #include "internal.h"
@@ -18,7 +21,7 @@ namespace lsh {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;   // head rows a thread has in flight
+constexpr int kAhead = 4;   // rows a thread has in flight
 
 struct RopeArgs {
   const void* in;
@@ -74,60 +77,104 @@ struct Pairs {
   }
 };
 
-template <class T, int P, bool INTER>
+// HB: heads of a token in flight; kAhead / HB tokens of a thread.
+template <class T, int P, bool INTER, int HB>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
-  const int n = a.tile * (int)a.fu.d;
+  constexpr int TB = kAhead / HB;
+  stream_wait();
+  let_next_start();
+  const int tt = (int)a.fu.div(threadIdx.x), u = (int)threadIdx.x - tt * (int)a.fu.d;
+  if (tt >= a.tile) return;
   const int h0 = blockIdx.y * a.heads, h1 = min(a.H, h0 + a.heads);
-  for (int j = threadIdx.x; j < n; j += kThreads) {
-    const int tt = (int)a.fu.div((uint32_t)j), u = j - tt * (int)a.fu.d;
-    const int t = blockIdx.x * a.tile + tt;
-    if (t >= a.tokens) return;
+  // second: from a pair's first feature to its second (copies: the next P)
+  const bool pair = u < a.pair_units;
+  const int c = pair ? u * (INTER ? 2 * P : P) : a.rot + (u - a.pair_units) * 2 * P;
+  const int second = pair ? a.half : P;
+  const int t0 = blockIdx.x * a.tile * TB + tt;
+  const T* in[TB];
+  T* out[TB];
+  int64_t pos[TB];
+#pragma unroll
+  for (int i = 0; i < TB; ++i) {
+    const int t = t0 + i * a.tile;
     const int b = (int)a.fl.div((uint32_t)t), l = t - b * a.L;
-    // second: from a pair's first feature to its second (copies: the next P)
-    const bool pair = u < a.pair_units;
-    const int c = pair ? u * (INTER ? 2 * P : P) : a.rot + (u - a.pair_units) * 2 * P;
-    const int second = pair ? a.half : P;
-    float cs[P], sn[P];
+    in[i] = (const T*)a.in + (b * a.si.b + l * a.si.l + c);
+    out[i] = (T*)a.out + (b * a.so.b + l * a.so.l + c);
+    pos[i] = a.pos0 + l;
+    if (a.pos && t < a.tokens)
+      pos[i] = a.pos0 + __ldg(a.pos + (int64_t)b * a.pos_batch * a.L + l);
+  }
+  Pairs<T, P, INTER> r[TB][HB];
+  auto load = [&](int h) {
 #pragma unroll
-    for (int i = 0; i < P; ++i) cs[i] = 1.f, sn[i] = 0.f;
+    for (int i = 0; i < TB; ++i)
+#pragma unroll
+      for (int k = 0; k < HB; ++k)
+        if (t0 + i * a.tile < a.tokens && h + k < h1) r[i][k].load(in[i] + (h + k) * a.si.h, second);
+  };
+  load(h0);   // on the way while the angles are formed
+  uint64_t turns[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) turns[i] = pair ? __ldg(a.turns + u * P + i) : 0;
+  float cs[TB == 1 ? P : 1], sn[TB == 1 ? P : 1];
+  auto angle = [&](int64_t at, int i, float& co, float& si) {
+    // half turns: 24 of the 32 bits survive, an angle error of pi 2^-25
+    const float x = (float)(int32_t)(((uint64_t)at * turns[i]) >> 32) * 0x1p-31f;
+    if constexpr (sizeof(T) == 2) __sincosf(x * 3.14159265f, &si, &co);
+    else sincospif(x, &si, &co);
+    co *= a.amp;
+    si *= a.amp * a.sign;
+  };
+  if constexpr (TB == 1) {
     if (pair) {
-      const int64_t pos = a.pos0 + (a.pos ? (int64_t)__ldg(a.pos + (int64_t)b * a.pos_batch * a.L + l)
-                                          : (int64_t)l);
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const uint64_t phase = (uint64_t)pos * __ldg(a.turns + u * P + i);
-        // half turns: 24 of the 32 bits survive, an angle error of pi 2^-25
-        sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &sn[i], &cs[i]);
-        cs[i] *= a.amp;
-        sn[i] *= a.amp * a.sign;
-      }
+      for (int i = 0; i < P; ++i) angle(pos[0], i, cs[i], sn[i]);
     }
-    const T* in = (const T*)a.in + (b * a.si.b + l * a.si.l + c);
-    T* out = (T*)a.out + (b * a.so.b + l * a.so.l + c);
-    for (int h = h0; h < h1; h += kAhead) {
-      Pairs<T, P, INTER> r[kAhead];
+    for (int h = h0; h < h1; h += HB) {
+      if (h != h0) load(h);
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k)
-        if (h + k < h1) r[k].load(in + (h + k) * a.si.h, second);
+      for (int k = 0; k < HB; ++k)
+        if (t0 < a.tokens && h + k < h1) {
+          if (pair) r[0][k].turn(cs, sn);
+          r[0][k].store(out[0] + (h + k) * a.so.h, second);
+        }
+    }
+  } else {
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k)
-        if (h + k < h1) {
-          if (pair) r[k].turn(cs, sn);
-          r[k].store(out + (h + k) * a.so.h, second);
+    for (int i = 0; i < TB; ++i) {
+      float c1[P], s1[P];
+      if (pair) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) angle(pos[i], p, c1[p], s1[p]);
+      }
+#pragma unroll
+      for (int k = 0; k < HB; ++k)
+        if (t0 + i * a.tile < a.tokens && h0 + k < h1) {
+          if (pair) r[i][k].turn(c1, s1);
+          r[i][k].store(out[i] + (h0 + k) * a.so.h, second);
         }
     }
   }
 }
 
+template <class T, int P, bool INTER, int HB>
+cudaError_t run_heads(const RopeArgs& a, cudaStream_t s) {
+  const int per = a.tile * (kAhead / HB);
+  note_launch();
+  return launch_overlapped(rope_kernel<T, P, INTER, HB>,
+                           dim3((unsigned)((a.tokens + per - 1) / per),
+                                (unsigned)((a.H + a.heads - 1) / a.heads)),
+                           kThreads, 0, s, a);
+}
 template <class T, int P, bool INTER>
-void run(const RopeArgs& a, cudaStream_t s) {
-  const dim3 grid((unsigned)((a.tokens + a.tile - 1) / a.tile),
-                  (unsigned)((a.H + a.heads - 1) / a.heads));
-  rope_kernel<T, P, INTER><<<grid, kThreads, 0, s>>>(a);
+cudaError_t run(const RopeArgs& a, cudaStream_t s) {
+  if (a.H == 1) return run_heads<T, P, INTER, 1>(a, s);
+  if (a.H == 2) return run_heads<T, P, INTER, 2>(a, s);
+  return run_heads<T, P, INTER, 4>(a, s);
 }
 template <class T, int P>
-void run_order(const RopeArgs& a, bool inter, cudaStream_t s) {
-  inter ? run<T, P, true>(a, s) : run<T, P, false>(a, s);
+cudaError_t run_order(const RopeArgs& a, bool inter, cudaStream_t s) {
+  return inter ? run<T, P, true>(a, s) : run<T, P, false>(a, s);
 }
 
 }  // namespace
@@ -152,17 +199,14 @@ cudaError_t launch_rope(const lsh_rope_problem& q, const lsh_strides& sin, const
                                           std::max<int64_t>(1, 148 * 8 / ctas));
   a.heads = (int)((q.H + split - 1) / split);
   if (q.dtype == LSH_BF16) {
-    if (vp == 8) run<__nv_bfloat16, 8, false>(a, s);
-    else if (vp == 4) run_order<__nv_bfloat16, 4>(a, q.interleaved, s);
-    else if (vp == 2) run_order<__nv_bfloat16, 2>(a, q.interleaved, s);
-    else run_order<__nv_bfloat16, 1>(a, q.interleaved, s);
-  } else {
-    if (vp == 4) run<float, 4, false>(a, s);
-    else if (vp == 2) run_order<float, 2>(a, q.interleaved, s);
-    else run_order<float, 1>(a, q.interleaved, s);
+    if (vp == 8) return run<__nv_bfloat16, 8, false>(a, s);
+    if (vp == 4) return run_order<__nv_bfloat16, 4>(a, q.interleaved, s);
+    if (vp == 2) return run_order<__nv_bfloat16, 2>(a, q.interleaved, s);
+    return run_order<__nv_bfloat16, 1>(a, q.interleaved, s);
   }
-  note_launch();
-  return cudaGetLastError();
+  if (vp == 4) return run<float, 4, false>(a, s);
+  if (vp == 2) return run_order<float, 2>(a, q.interleaved, s);
+  return run_order<float, 1>(a, q.interleaved, s);
 }
 
 }  // namespace lsh

@@ -8,6 +8,30 @@
 
 namespace lsh {
 
+// Programmatic dependent launch: a kernel of this file's users lets the next
+// one of the stream be set up while it runs, and waits for all earlier work of
+// the stream before it touches memory. Every thread of every kernel waits, so
+// that the end of a kernel means the end of all before it.
+__device__ __forceinline__ void stream_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <class Args>
+cudaError_t launch_overlapped(void (*fn)(const Args), dim3 grid, unsigned threads, size_t smem,
+                              cudaStream_t s, const Args& a) {
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, fn, a);
+}
+
 // V consecutive elements of type T as 32-bit words (one half word for V = 1
 // bf16), loaded and stored in accesses of at most 16 bytes.
 template <class T, int V>
