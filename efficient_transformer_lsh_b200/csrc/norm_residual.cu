@@ -9,6 +9,7 @@ static int max_parts(int all, int groups) { return std::max(1, all / std::max(1,
 
 SubShape sub_shape(const SubCall& c, const SubSize& z) {
   SubShape s{};
+  s.vecs = z.vecs;
   const int D = c.H * c.d, esize = c.dtype == LSH_BF16 ? 2 : 4;
   s.groups = c.gate_batch ? c.B : 1;
   s.tokens = c.gate_batch ? c.L : c.B * c.L;
@@ -34,12 +35,12 @@ SubShape sub_shape(const SubCall& c, const SubSize& z) {
     // pays where a branch makes many (4 x 4096 x 4096, everything on: 238 us
     // against 307), but a norm alone gains more from twice the warps (196
     // against 247); 512 threads of two tokens do not fit the register file.
-    if (s.team > 256 || (s.team > 32 && !c.branch)) s.tok = 1;
+    if (z.backward && (s.team > 256 || (s.team > 32 && !c.branch))) s.tok = 1;
     s.teams = std::max(1, threads / s.team);
     s.threads = s.teams * s.team;
     // threads resident on an SM, by the registers of each form
     int room = 512;
-    if (s.wide && s.team > 32 && z.tok > 1) room = s.tok > 1 ? 256 : 512;
+    if (z.backward && s.wide && s.team > 32 && z.tok > 1) room = s.tok > 1 ? 256 : 512;
     else if (s.wide) room = z.ctas * threads;
     ctas = std::max(1, room / s.threads);
     const int fixed = z.vecs * per * 4 * s.team + (s.team > 32 ? s.teams * 64 * kMaxWarps : 0);
@@ -77,7 +78,7 @@ SubArgs sub_args(const SubCall& c, const SubShape& s) {
   a.units = a.D / V;
   a.gpr = (c.d + 7) / 8;
   a.tokens = s.tokens, a.parts = s.parts;
-  a.team = s.team, a.teams = s.teams, a.stages = s.stages;
+  a.team = s.team, a.teams = s.teams, a.stages = s.stages, a.vecs = s.vecs;
   a.post = c.post, a.norm = c.norm, a.gate = c.gate, a.gate_batch = c.gate_batch;
   a.eps_post = c.eps_post, a.eps = c.eps, a.alpha = c.alpha, a.beta = c.beta;
   a.inv_d = 1.f / (float)a.D;
@@ -90,7 +91,8 @@ SubArgs sub_args(const SubCall& c, const SubShape& s) {
 cudaError_t launch_sub_fwd(const SubCall& c, cudaStream_t st) {
   const SubShape s = sub_shape(c, {kFwdPer, 1, kFwdThreads,
                                    1 + c.branch + (c.gate == LSH_GATE_SIGMOID),
-                                   c.branch ? 4 : 2, c.branch ? kFwdCtas : kFwdNormCtas});
+                                   (c.branch ? 2 : 1) * (c.b || c.bp ? 2 : 1),
+                                   c.branch ? kFwdCtas : kFwdNormCtas, false});
   const SubArgs a = sub_args(c, s);
   return c.dtype == LSH_BF16 ? sub_fwd_type<__nv_bfloat16>(c, a, s, st)
                              : sub_fwd_type<float>(c, a, s, st);
@@ -161,11 +163,18 @@ __global__ void __launch_bounds__(1024) sub_final_kernel(const FinalArgs a) {
   }
 }
 
-template <class T>
+template <class T, bool SIG>
+cudaError_t run_bwd(const SubCall& c, const SubArgs& a, const SubShape& s, cudaStream_t st) {
+  return c.norm != LSH_NORM_NONE ? sub_bwd_type<T, true, SIG>(c, a, s, st)
+                                 : sub_bwd_type<T, false, SIG>(c, a, s, st);
+}
+
+template <class T, bool SIG>
 SubShape bwd_shape(const SubCall& c, int tensors) {
-  using Z = BwdSize<T>;
-  return sub_shape(c, {kBwdPer, Z::kTok, Z::kThreads, tensors,
-                       (c.norm != LSH_NORM_NONE) + 2 * c.branch, Z::kCtas});
+  using Z = BwdSize<T, SIG>;
+  const int norm = c.norm != LSH_NORM_NONE;
+  return sub_shape(c, {kBwdPer, Z::kTok, Z::kThreads, tensors, norm + c.branch + (SIG && c.bp),
+                       Z::kCtas, true});
 }
 
 }  // namespace
@@ -181,19 +190,21 @@ size_t sub_bwd_ws_bytes(int B, int H, int L, int d, bool branch, bool gate_batch
 cudaError_t launch_sub_bwd(const SubCall& c, void* ws, cudaStream_t st) {
   const bool norm = c.norm != LSH_NORM_NONE;
   const int tensors = 2 * norm + (c.dy != nullptr) + c.branch + (c.gate == LSH_GATE_SIGMOID);
-  const SubShape s = c.dtype == LSH_BF16 ? bwd_shape<__nv_bfloat16>(c, tensors)
-                                         : bwd_shape<float>(c, tensors);
+  const bool sig = c.gate == LSH_GATE_SIGMOID, bf16 = c.dtype == LSH_BF16;
+  const SubShape s = bf16 ? sig ? bwd_shape<__nv_bfloat16, true>(c, tensors)
+                                : bwd_shape<__nv_bfloat16, false>(c, tensors)
+                     : sig ? bwd_shape<float, true>(c, tensors)
+                           : bwd_shape<float, false>(c, tensors);
   SubArgs a = sub_args(c, s);
   const bool sums = c.dgate || c.dwp || c.dbp || c.dw || c.db;
   a.part = sums ? (float*)ws : nullptr;
   if ((int64_t)c.B * c.L == 0 && !sums) return cudaSuccess;
   if ((int64_t)c.B * c.L > 0) {
     cudaError_t e;
-    if (c.dtype == LSH_BF16)
-      e = norm ? sub_bwd_type<__nv_bfloat16, true>(c, a, s, st)
-               : sub_bwd_type<__nv_bfloat16, false>(c, a, s, st);
-    else
-      e = norm ? sub_bwd_type<float, true>(c, a, s, st) : sub_bwd_type<float, false>(c, a, s, st);
+    e = bf16 ? sig ? run_bwd<__nv_bfloat16, true>(c, a, s, st)
+                   : run_bwd<__nv_bfloat16, false>(c, a, s, st)
+        : sig ? run_bwd<float, true>(c, a, s, st)
+              : run_bwd<float, false>(c, a, s, st);
     if (e != cudaSuccess || !sums) return e;
   }
   FinalArgs f{};

@@ -52,7 +52,7 @@ struct SubArgs {
   int H, L, D, units, gpr;
   int tokens, parts;      // tokens of a group; CTAs of a group
   int team, teams;        // threads of a team; teams of a CTA
-  int stages;             // of the ring
+  int stages, vecs;       // of the ring; parameter vectors in shared memory
   int post, norm, gate, gate_batch;
   float eps_post, eps, alpha, beta, inv_d;
   uint32_t drop_t;
@@ -166,7 +166,7 @@ __device__ __forceinline__ void cp_wait_for(int pending) {
 // neighbouring ones; `live` is false for a token past the last, which a team
 // only goes along with.
 // TEAM: threads of a token up to a warp, or 0: whole warps, a.team threads.
-template <class T, int V, int PER, int TEAM, int NVEC, int TOK, int THREADS>
+template <class T, int V, int PER, int TEAM, int TOK, int THREADS>
 struct Place {
   static constexpr bool kMulti = TEAM == 0;
   static constexpr int NV = PER / V;
@@ -199,7 +199,7 @@ struct Place {
       }
     }
     par = (uint32_t)__cvta_generic_to_shared(smem) + lane * 16;
-    unsigned char* p = smem + NVEC * (PER / 4) * team() * 16;
+    unsigned char* p = smem + a.vecs * (PER / 4) * team() * 16;
     red = reinterpret_cast<float*>(p) + team_id * (16 * kMaxWarps);
     if (kMulti) p += a.teams * (64 * kMaxWarps);
     ring = (uint32_t)__cvta_generic_to_shared(p) + threadIdx.x * 16;
@@ -444,6 +444,22 @@ struct Place {
     }
   }
 
+  // v = v p + q
+  template <int N>
+  __device__ __forceinline__ void scale_shift(int vp, int vq, f2 (&v)[N][P]) const {
+#pragma unroll
+    for (int j = 0; j < PER / 4; ++j) {
+      f2 lo, hi, blo, bhi;
+      params(vp, j, lo, hi);
+      params(vq, j, blo, bhi);
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        v[n][2 * j] = fma2(v[n][2 * j], lo, blo);
+        v[n][2 * j + 1] = fma2(v[n][2 * j + 1], hi, bhi);
+      }
+    }
+  }
+
   // ---- dropout: kept values times m, others 0 ----
   __device__ __forceinline__ void drop_all(uint64_t offset, int b, int l, float m,
                                            f2 (&v)[P]) const {
@@ -499,11 +515,12 @@ __device__ __forceinline__ float inv_std(float sum_sq, float inv_d, float eps) {
 // one stage has to fit, and a token's vectors have to lie within 2^31 elements
 // of its first.
 struct SubShape {
-  int team, teams, threads, tok, groups, tokens, parts, stages, smem;
+  int team, teams, threads, tok, groups, tokens, parts, stages, vecs, smem;
   bool wide;
 };
 struct SubSize {
   int per, tok, threads, tensors, vecs, ctas;   // of the wide kernel
+  bool backward;
 };
 SubShape sub_shape(const SubCall& c, const SubSize& z);
 SubArgs sub_args(const SubCall& c, const SubShape& s);
@@ -526,20 +543,23 @@ cudaError_t with_team(int team, F f) {
 // of an SM, for the wide kernels. Forward: 32 features, so that a warp takes
 // two tokens of 512. Backward: the four sums of parameter gradients already
 // take four registers a feature, so 16 features, and two tokens at a time in
-// bf16; in float32, where a token is twice the bytes, one.
+// bf16; one in float32, where a token is twice the bytes, and with a sigmoid
+// gate, whose registers for two would spill (64K x 512 features: 207 us
+// against 155).
 constexpr int kFwdPer = 32, kFwdThreads = 256, kFwdCtas = 2, kFwdNormCtas = 3;
 constexpr int kBwdPer = 16;
 constexpr int kNarrowThreads = 256;
-template <class T>
+template <class T, bool SIG>
 struct BwdSize {
-  static constexpr int kTok = sizeof(T) == 2 ? 2 : 1;
-  static constexpr int kThreads = sizeof(T) == 2 ? 128 : 256;
-  static constexpr int kCtas = sizeof(T) == 2 ? 3 : 2;
+  static constexpr bool kTwo = sizeof(T) == 2 && !SIG;
+  static constexpr int kTok = kTwo ? 2 : 1;
+  static constexpr int kThreads = kTwo ? 128 : 256;
+  static constexpr int kCtas = kTwo ? 3 : 2;
 };
 
 template <class T>
 cudaError_t sub_fwd_type(const SubCall& c, const SubArgs& a, const SubShape& s, cudaStream_t st);
-template <class T, bool NORM>
+template <class T, bool NORM, bool SIG>
 cudaError_t sub_bwd_type(const SubCall& c, const SubArgs& a, const SubShape& s, cudaStream_t st);
 
 // CTAs of a call, and so rows of partial sums of a backward one, at most.

@@ -1,6 +1,6 @@
 // Backward kernel of the norms and the residual add; see norm_residual.cuh.
-// Instantiated for each element type, with and without a norm of y, in a file
-// of its own.
+// Instantiated for each element type, with and without a norm of y and a
+// sigmoid gate, in a file of its own.
 //
 // Parameter gradients are sums over tokens. Every thread keeps its features'
 // sums in registers over all the tokens it visits; a CTA writes one row of
@@ -48,14 +48,13 @@ __device__ __forceinline__ void write_part(const At& at, const f2 (&s)[At::P], f
 // Parameters, in order: W, P1 = gate w_post (a sigmoid gate is not in it), P0
 // = b_post (sigmoid gates only).
 template <class T, int V, int PER, int TEAM, int TOK, bool BRANCH, bool NORM, bool POST, bool SIG>
-__global__ void __launch_bounds__(TEAM != 0  ? (V == 1 ? kNarrowThreads : BwdSize<T>::kThreads)
+__global__ void __launch_bounds__(TEAM != 0  ? (V == 1 ? kNarrowThreads : BwdSize<T, SIG>::kThreads)
                                   : TOK == 1 ? 32 * kMaxWarps
                                              : 256,
-                                  TEAM != 0 ? (V == 1 ? 2 : BwdSize<T>::kCtas) : 1)
+                                  TEAM != 0 ? (V == 1 ? 2 : BwdSize<T, SIG>::kCtas) : 1)
 sub_bwd_kernel(const __grid_constant__ SubArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
-  using At = Place<T, V, PER, TEAM, (NORM ? 1 : 0) + (BRANCH ? 2 : 0), TOK,
-                   V == 1 ? kNarrowThreads : BwdSize<T>::kThreads>;
+  using At = Place<T, V, PER, TEAM, TOK, V == 1 ? kNarrowThreads : BwdSize<T, SIG>::kThreads>;
   constexpr int P = At::P;
   constexpr int kP1 = NORM ? 1 : 0, kP0 = kP1 + 1;
   At at(a, smem);
@@ -318,14 +317,11 @@ sub_bwd_kernel(const __grid_constant__ SubArgs a) {
   }
 }
 
-template <class T, int V, int PER, int TEAM, int TOK, bool NORM>
+template <class T, int V, int PER, int TEAM, int TOK, bool NORM, bool SIG>
 cudaError_t run_branch(const SubCall& c, const SubArgs& a, const SubShape& s, cudaStream_t st) {
-  const bool sig = c.gate == LSH_GATE_SIGMOID, post = c.post != LSH_NORM_NONE;
-  auto fn = post && sig ? sub_bwd_kernel<T, V, PER, TEAM, TOK, true, NORM, true, true>
-            : post      ? sub_bwd_kernel<T, V, PER, TEAM, TOK, true, NORM, true, false>
-            : sig       ? sub_bwd_kernel<T, V, PER, TEAM, TOK, true, NORM, false, true>
-                        : sub_bwd_kernel<T, V, PER, TEAM, TOK, true, NORM, false, false>;
-  if constexpr (NORM)
+  auto fn = c.post != LSH_NORM_NONE ? sub_bwd_kernel<T, V, PER, TEAM, TOK, true, NORM, true, SIG>
+                                    : sub_bwd_kernel<T, V, PER, TEAM, TOK, true, NORM, false, SIG>;
+  if constexpr (NORM && !SIG)
     if (!c.branch) fn = sub_bwd_kernel<T, V, PER, TEAM, TOK, false, true, false, false>;
   // the row of partial sums goes through the same memory
   const int smem = std::max(s.smem, s.teams * a.D * 4);
@@ -340,16 +336,16 @@ cudaError_t run_branch(const SubCall& c, const SubArgs& a, const SubShape& s, cu
 
 }  // namespace
 
-template <class T, bool NORM>
+template <class T, bool NORM, bool SIG>
 cudaError_t sub_bwd_type(const SubCall& c, const SubArgs& a, const SubShape& s, cudaStream_t st) {
-  constexpr int V = 16 / (int)sizeof(T), TOK = BwdSize<T>::kTok;
-  if (s.wide && s.tok < TOK) return run_branch<T, V, kBwdPer, 0, 1, NORM>(c, a, s, st);
+  constexpr int V = 16 / (int)sizeof(T), TOK = BwdSize<T, SIG>::kTok;
+  if (s.wide && s.tok < TOK) return run_branch<T, V, kBwdPer, 0, 1, NORM, SIG>(c, a, s, st);
   if (s.wide)
     return with_team(s.team, [&](auto t) {
-      return run_branch<T, V, kBwdPer, t.value, TOK, NORM>(c, a, s, st);
+      return run_branch<T, V, kBwdPer, t.value, TOK, NORM, SIG>(c, a, s, st);
     });
-  return s.team == 32 ? run_branch<T, 1, kNarrowPer, 32, 1, NORM>(c, a, s, st)
-                      : run_branch<T, 1, kNarrowPer, 0, 1, NORM>(c, a, s, st);
+  return s.team == 32 ? run_branch<T, 1, kNarrowPer, 32, 1, NORM, SIG>(c, a, s, st)
+                      : run_branch<T, 1, kNarrowPer, 0, 1, NORM, SIG>(c, a, s, st);
 }
 
 }  // namespace lsh

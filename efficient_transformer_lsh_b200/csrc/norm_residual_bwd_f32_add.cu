@@ -1,6 +1,6 @@
 #include "norm_residual_bwd.cuh"
 
 namespace lsh {
-template cudaError_t sub_bwd_type<float, false>(const SubCall&, const SubArgs&, const SubShape&,
-                                            cudaStream_t);
+template cudaError_t sub_bwd_type<float, false, false>(const SubCall&, const SubArgs&, const SubShape&,
+                                                  cudaStream_t);
 }  // namespace lsh

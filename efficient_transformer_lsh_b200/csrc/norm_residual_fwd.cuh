@@ -7,16 +7,17 @@
 namespace lsh {
 namespace {
 
-// Parameters, in order: P1 = gate w_post, P0 = gate b_post (a sigmoid gate is
-// not in them), W, B: the products are formed once a CTA, not once a token.
-template <class T, int V, int PER, int TEAM, bool BRANCH, bool POST, bool SIG>
+// Parameters, in order: W, P1 = gate w_post (a sigmoid gate is not in it), then
+// B, P0 = gate b_post where there is one of them: the products are formed once
+// a CTA, not once a token.
+template <class T, int V, int PER, int TEAM, int TOK, bool BRANCH, bool POST, bool SIG>
 __global__ void __launch_bounds__(V == 1 ? 32 * kMaxWarps : kFwdThreads,
                                   V == 1   ? 1
                                   : BRANCH ? kFwdCtas
                                            : kFwdNormCtas)
 sub_fwd_kernel(const __grid_constant__ SubArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
-  using At = Place<T, V, PER, TEAM, BRANCH ? 4 : 2, 1, V == 1 ? kNarrowThreads : kFwdThreads>;
+  using At = Place<T, V, PER, TEAM, TOK, V == 1 ? kNarrowThreads : kFwdThreads>;
   constexpr int P = At::P;
   At at(a, smem);
   stream_wait();
@@ -25,32 +26,35 @@ sub_fwd_kernel(const __grid_constant__ SubArgs a) {
   const bool norm = a.norm != LSH_NORM_NONE;
   const float* gv = a.gv ? a.gv + (int64_t)at.group * (a.gate_batch ? a.D : 0) : nullptr;
   const bool has1 = BRANCH && (a.wp || gv), has0 = BRANCH && a.bp;
-  constexpr int kW = BRANCH ? 2 : 0, kB = kW + 1;
-  if (has1) at.stage_param(0, a.wp, gv);
-  if (has0) at.stage_param(1, a.bp, gv);
-  if (norm && a.w) at.stage_param(kW, a.w, nullptr);
+  constexpr int kW = 0, kP1 = 1, kB = BRANCH ? 2 : 1, kP0 = 3;
+  if (norm && (a.w || a.b)) at.stage_param(kW, a.w, nullptr);
+  if (has1 || has0) at.stage_param(kP1, a.wp, gv);
   if (norm && a.b) at.stage_param(kB, a.b, nullptr);
+  if (has0) at.stage_param(kP0, a.bp, gv);
   const int tensors = 1 + BRANCH + sig;
-  at.clear(at.ring, a.stages * tensors);
+  at.clear(at.ring, a.stages * tensors * TOK);
   __syncthreads();
   const uint64_t offset = a.offset + (a.counter ? __ldg(a.counter) : 0);
   const int step = at.step(), rounds = at.rounds();
-  const uint32_t stage_bytes = tensors * at.one();
+  const uint32_t one = at.one(), token_bytes = tensors * one, stage_bytes = TOK * token_bytes;
 
   int t_in = at.first(), n_in = 0;
-  uint32_t s_in = at.ring;      // where the next token's copies go
+  uint32_t s_in = at.ring;      // where the next tokens' copies go
   auto copy = [&]() {
     if constexpr (At::kRing) {
       if (n_in < rounds) {
-        if (t_in < a.tokens) {
-          int b, l;
-          at.token(t_in, b, l);
-          const int64_t rx = At::row(a.sx, b, l);
-          at.issue(a.x, at.ox, rx, s_in);
-          if constexpr (BRANCH) {
-            const int64_t rf = At::row(a.sf, b, l);
-            at.issue(a.f, at.of, rf, s_in + at.one());
-            if (sig) at.issue(a.z, at.of, rf, s_in + 2 * at.one());
+#pragma unroll
+        for (int j = 0; j < TOK; ++j) {
+          const uint32_t to = s_in + j * token_bytes;
+          if (t_in + j < a.tokens) {
+            int b, l;
+            at.token(t_in + j, b, l);
+            at.issue(a.x, at.ox, At::row(a.sx, b, l), to);
+            if constexpr (BRANCH) {
+              const int64_t rf = At::row(a.sf, b, l);
+              at.issue(a.f, at.of, rf, to + one);
+              if (sig) at.issue(a.z, at.of, rf, to + 2 * one);
+            }
           }
         }
         t_in += step;
@@ -67,66 +71,77 @@ sub_fwd_kernel(const __grid_constant__ SubArgs a) {
   for (int n = 0; n < rounds; ++n, t += step) {
     copy();
     if constexpr (At::kRing) cp_wait_for(a.stages - 1);
-    const bool live = At::kMulti || t < a.tokens;
-    int b, l;
-    at.token(t, b, l);
-    f2 row[1][P];
-    f2(&v)[P] = row[0];
-    if constexpr (BRANCH) {
-      at.get(a.f, a.sf, b, l, live, st + at.one(), v);
-      if (post) {
-        float s[1];
-        if (a.post == LSH_NORM_LAYER) {
-          s[0] = sum_all(v);
-          at.team_sum(s);
-          at.center(v, s[0] * a.inv_d);
-        }
-        s[0] = dot_all(v, v);
+    int b[TOK], l[TOK];
+    bool live[TOK];
+#pragma unroll
+    for (int j = 0; j < TOK; ++j) {
+      live[j] = (At::kMulti && TOK == 1) || t + j < a.tokens;
+      at.token(t + j, b[j], l[j]);
+    }
+    auto get = [&](const void* p, const lsh_strides& s, int i, int j, f2(&v)[P]) {
+      at.get(p, s, b[j], l[j], live[j], st + j * token_bytes + i * one, v);
+    };
+    f2 v[TOK][P];
+    // v -> xhat of each token
+    auto normalize = [&](int kind, float eps) {
+      float s[TOK];
+      if (kind == LSH_NORM_LAYER) {
+#pragma unroll
+        for (int j = 0; j < TOK; ++j) s[j] = sum_all(v[j]);
         at.team_sum(s);
-        scale_all(v, inv_std(s[0], a.inv_d, a.eps_post));
-      }
-      if (has1) at.scale_by(0, row);
-      if (has0) at.shift_by(1, row);
-      if (sig) {
-        f2 z[P];
-        at.get(a.z, a.sf, b, l, live, st + 2 * at.one(), z);
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-          const float2 u = up(z[i]);
-          float slope;
-          const float g0 = sigmoid(u.x, slope), g1 = sigmoid(u.y, slope);
-          v[i] = mul2(v[i], pk(g0, g1));
+        for (int j = 0; j < TOK; ++j) at.center(v[j], s[j] * a.inv_d);
+      }
+#pragma unroll
+      for (int j = 0; j < TOK; ++j) s[j] = dot_all(v[j], v[j]);
+      at.team_sum(s);
+#pragma unroll
+      for (int j = 0; j < TOK; ++j) scale_all(v[j], inv_std(s[j], a.inv_d, eps));
+    };
+    if constexpr (BRANCH) {
+#pragma unroll
+      for (int j = 0; j < TOK; ++j) get(a.f, a.sf, 1, j, v[j]);
+      if (post) normalize(a.post, a.eps_post);
+      if (has0) at.scale_shift(kP1, kP0, v);
+      else if (has1) at.scale_by(kP1, v);
+      if constexpr (sig) {
+#pragma unroll
+        for (int j = 0; j < TOK; ++j) {
+          f2 z[P];
+          get(a.z, a.sf, 2, j, z);
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            const float2 u = up(z[i]);
+            float slope;
+            const float g0 = sigmoid(u.x, slope), g1 = sigmoid(u.y, slope);
+            v[j][i] = mul2(v[j][i], pk(g0, g1));
+          }
         }
       }
-      float m = a.alpha;
-      if (a.drop_t) {
-        at.drop_all(offset, b, l, m * a.drop_scale, v);
-        m = 1.f;
-      }
-      f2 x[P];
-      at.get(a.x, a.sx, b, l, live, st, x);
-      const f2 m2 = pk(m, m), beta = pk(a.beta, a.beta);
 #pragma unroll
-      for (int i = 0; i < P; ++i) v[i] = fma2(v[i], m2, mul2(x[i], beta));
-      // v becomes the row as stored: h is the same whether it comes from here
-      // or from a later pass over y
-      at.template put<true>(a.y, a.sx, at.ox, b, l, live, v);
+      for (int j = 0; j < TOK; ++j) {
+        if (a.drop_t) at.drop_all(offset, b[j], l[j], a.alpha * a.drop_scale, v[j]);
+        else scale_all(v[j], a.alpha);
+        f2 x[P];
+        get(a.x, a.sx, 0, j, x);
+        const f2 beta = pk(a.beta, a.beta);
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[j][i] = fma2(x[i], beta, v[j][i]);
+        // v becomes the row as stored: h is the same whether it comes from
+        // here or from a later pass over y
+        at.template put<true>(a.y, a.sx, at.ox, b[j], l[j], live[j], v[j]);
+      }
     } else {
-      at.get(a.x, a.sx, b, l, live, st, v);
+#pragma unroll
+      for (int j = 0; j < TOK; ++j) get(a.x, a.sx, 0, j, v[j]);
     }
     if (norm) {
-      float s[1];
-      if (a.norm == LSH_NORM_LAYER) {
-        s[0] = sum_all(v);
-        at.team_sum(s);
-        at.center(v, s[0] * a.inv_d);
-      }
-      s[0] = dot_all(v, v);
-      at.team_sum(s);
-      scale_all(v, inv_std(s[0], a.inv_d, a.eps));
-      if (a.w) at.scale_by(kW, row);
-      if (a.b) at.shift_by(kB, row);
-      at.template put<false>(a.h, a.sh, BRANCH ? at.ox : at.oh, b, l, live, v);
+      normalize(a.norm, a.eps);
+      if (a.b) at.scale_shift(kW, kB, v);
+      else if (a.w) at.scale_by(kW, v);
+#pragma unroll
+      for (int j = 0; j < TOK; ++j)
+        at.template put<false>(a.h, a.sh, BRANCH ? at.ox : at.oh, b[j], l[j], live[j], v[j]);
     }
     st += stage_bytes;
     if (st == at.ring + a.stages * stage_bytes) st = at.ring;
@@ -134,14 +149,14 @@ sub_fwd_kernel(const __grid_constant__ SubArgs a) {
   if constexpr (At::kRing) cp_wait<0>();
 }
 
-template <class T, int V, int PER, int TEAM>
+template <class T, int V, int PER, int TEAM, int TOK>
 cudaError_t run(const SubCall& c, const SubArgs& a, const SubShape& s, cudaStream_t st) {
   const bool sig = c.gate == LSH_GATE_SIGMOID, post = c.post != LSH_NORM_NONE;
-  auto fn = !c.branch     ? sub_fwd_kernel<T, V, PER, TEAM, false, false, false>
-            : post && sig ? sub_fwd_kernel<T, V, PER, TEAM, true, true, true>
-            : post        ? sub_fwd_kernel<T, V, PER, TEAM, true, true, false>
-            : sig         ? sub_fwd_kernel<T, V, PER, TEAM, true, false, true>
-                          : sub_fwd_kernel<T, V, PER, TEAM, true, false, false>;
+  auto fn = !c.branch     ? sub_fwd_kernel<T, V, PER, TEAM, TOK, false, false, false>
+            : post && sig ? sub_fwd_kernel<T, V, PER, TEAM, TOK, true, true, true>
+            : post        ? sub_fwd_kernel<T, V, PER, TEAM, TOK, true, true, false>
+            : sig         ? sub_fwd_kernel<T, V, PER, TEAM, TOK, true, false, true>
+                          : sub_fwd_kernel<T, V, PER, TEAM, TOK, true, false, false>;
   if (s.smem > kSmemDefault) {
     cudaError_t e =
         cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerSm);
@@ -157,10 +172,10 @@ template <class T>
 cudaError_t sub_fwd_type(const SubCall& c, const SubArgs& a, const SubShape& s, cudaStream_t st) {
   if (s.wide)
     return with_team(s.team, [&](auto t) {
-      return run<T, 16 / (int)sizeof(T), kFwdPer, t.value>(c, a, s, st);
+      return run<T, 16 / (int)sizeof(T), kFwdPer, t.value, 1>(c, a, s, st);
     });
-  return s.team == 32 ? run<T, 1, kNarrowPer, 32>(c, a, s, st)
-                      : run<T, 1, kNarrowPer, 0>(c, a, s, st);
+  return s.team == 32 ? run<T, 1, kNarrowPer, 32, 1>(c, a, s, st)
+                      : run<T, 1, kNarrowPer, 0, 1>(c, a, s, st);
 }
 
 }  // namespace lsh
