@@ -29,7 +29,7 @@ EXPORTS = ("lsh_hash", "lsh_sort_workspace_size", "lsh_sort", "lsh_fwd_workspace
            "lsh_rev_fwd_workspace_size", "lsh_rev_fwd", "lsh_rev_bwd_workspace_size",
            "lsh_rev_bwd", "lsh_norm_fwd", "lsh_norm_bwd_workspace_size", "lsh_norm_bwd",
            "lsh_dropout_fwd", "lsh_residual_fwd", "lsh_residual_bwd_workspace_size",
-           "lsh_residual_bwd", "lsh_rope_fwd", "lsh_rope_bwd")
+           "lsh_residual_bwd", "lsh_rope_fwd", "lsh_rope_bwd", "lsh_rope_bwd_sum")
 # Size of the library-owned scratch used by lsh_sort_noalloc (matches lsh.h).
 SORT_NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 
@@ -180,6 +180,7 @@ def lib() -> ctypes.CDLL:
             "lsh_residual_bwd": ([S] + [vp] * 8 + [u64, u64] + [vp] * 9 + [sz, vp],
                                  ctypes.c_int),
             "lsh_rope_fwd": ([E, vp, vp, vp, ctypes.c_int64, vp, vp], ctypes.c_int),
+            "lsh_rope_bwd_sum": ([E, vp, vp, vp, vp, ctypes.c_int64, vp, vp], ctypes.c_int),
             "lsh_rope_bwd": ([E, vp, vp, vp, ctypes.c_int64, vp, vp], ctypes.c_int),
         }
         for name, (args, res) in sig.items():
@@ -321,7 +322,7 @@ def lsh_rev_bwd(p: lsh_problem, f: lsh_ff_problem, y1, y2, dy1, dy2, perm, W1, b
                              _ptr(dW2), _ptr(db2), _ptr(ws), int(ws_bytes), _stream(stream)),
            "lsh_rev_bwd", "lsh_norm_fwd", "lsh_norm_bwd_workspace_size", "lsh_norm_bwd",
            "lsh_dropout_fwd", "lsh_residual_fwd", "lsh_residual_bwd_workspace_size",
-           "lsh_residual_bwd", "lsh_rope_fwd", "lsh_rope_bwd")
+           "lsh_residual_bwd", "lsh_rope_fwd", "lsh_rope_bwd", "lsh_rope_bwd_sum")
 
 
 def lsh_device_status(stream=None) -> int:
@@ -388,3 +389,8 @@ def lsh_rope_fwd(q: lsh_rope_problem, x, turns, pos, pos0: int, y, stream=None):
 def lsh_rope_bwd(q: lsh_rope_problem, dy, turns, pos, pos0: int, dx, stream=None):
     _check(lib().lsh_rope_bwd(ctypes.byref(q), _ptr(dy), _ptr(turns), _ptr(pos), int(pos0),
                               _ptr(dx), _stream(stream)), "lsh_rope_bwd")
+
+
+def lsh_rope_bwd_sum(q: lsh_rope_problem, dqk, dv, turns, pos, pos0: int, dx, stream=None):
+    _check(lib().lsh_rope_bwd_sum(ctypes.byref(q), _ptr(dqk), _ptr(dv), _ptr(turns), _ptr(pos),
+                                  int(pos0), _ptr(dx), _stream(stream)), "lsh_rope_bwd_sum")

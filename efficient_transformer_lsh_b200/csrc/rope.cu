@@ -25,6 +25,7 @@ constexpr int kAhead = 4;   // rows a thread has in flight
 
 struct RopeArgs {
   const void* in;
+  const float* add;        // the sum's second term
   void* out;
   lsh_strides si, so;
   const uint64_t* turns;
@@ -50,32 +51,57 @@ struct Pairs {
     a.store(p);
     if constexpr (!INTER) b.store(p + second);
   }
-  __device__ __forceinline__ void turn(const float (&c)[P], const float (&s)[P]) {
+  // firsts and seconds of the pairs (copied features: any split)
+  __device__ __forceinline__ void get(float (&p)[P], float (&q)[P]) const {
     if constexpr (INTER) {
       float v[2 * P];
       a.get(v);
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const float p = v[2 * i], q = v[2 * i + 1];
-        v[2 * i] = p * c[i] - q * s[i];
-        v[2 * i + 1] = q * c[i] + p * s[i];
-      }
+      for (int i = 0; i < P; ++i) p[i] = v[2 * i], q[i] = v[2 * i + 1];
+    } else {
+      a.get(p);
+      b.get(q);
+    }
+  }
+  __device__ __forceinline__ void set(const float (&p)[P], const float (&q)[P]) {
+    if constexpr (INTER) {
+      float v[2 * P];
+#pragma unroll
+      for (int i = 0; i < P; ++i) v[2 * i] = p[i], v[2 * i + 1] = q[i];
       a.set(v);
     } else {
-      float v[P], u[P];
-      a.get(v);
-      b.get(u);
+      a.set(p);
+      b.set(q);
+    }
+  }
+  __device__ __forceinline__ void turn(const float (&c)[P], const float (&s)[P]) {
+    float p[P], q[P];
+    get(p, q);
+    turn_pairs(p, q, c, s);
+    set(p, q);
+  }
+  static __device__ __forceinline__ void turn_pairs(float (&p)[P], float (&q)[P],
+                                                    const float (&c)[P], const float (&s)[P]) {
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const float p = v[i], q = u[i];
-        v[i] = p * c[i] - q * s[i];
-        u[i] = q * c[i] + p * s[i];
-      }
-      a.set(v);
-      b.set(u);
+    for (int i = 0; i < P; ++i) {
+      const float u = p[i], v = q[i];
+      p[i] = u * c[i] - v * s[i];
+      q[i] = v * c[i] + u * s[i];
     }
   }
 };
+
+// Sine and cosine, times amp, of the angle at a position.
+template <bool FAST>
+__device__ __forceinline__ void angle(const RopeArgs& a, int64_t pos, uint64_t turns, float& co,
+                                      float& si) {
+  // half turns: 24 of the 32 bits survive, an angle error of pi 2^-25
+  const float x = (float)(int32_t)(((uint64_t)pos * turns) >> 32) * 0x1p-31f;
+  if constexpr (FAST) __sincosf(x * 3.14159265f, &si, &co);
+  else sincospif(x, &si, &co);
+  co *= a.amp;
+  si *= a.amp * a.sign;
+}
 
 // HB: heads of a token in flight; kAhead / HB tokens of a thread.
 template <class T, int P, bool INTER, int HB>
@@ -117,18 +143,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 #pragma unroll
   for (int i = 0; i < P; ++i) turns[i] = pair ? __ldg(a.turns + u * P + i) : 0;
   float cs[TB == 1 ? P : 1], sn[TB == 1 ? P : 1];
-  auto angle = [&](int64_t at, int i, float& co, float& si) {
-    // half turns: 24 of the 32 bits survive, an angle error of pi 2^-25
-    const float x = (float)(int32_t)(((uint64_t)at * turns[i]) >> 32) * 0x1p-31f;
-    if constexpr (sizeof(T) == 2) __sincosf(x * 3.14159265f, &si, &co);
-    else sincospif(x, &si, &co);
-    co *= a.amp;
-    si *= a.amp * a.sign;
-  };
+  constexpr bool kFast = sizeof(T) == 2;
   if constexpr (TB == 1) {
     if (pair) {
 #pragma unroll
-      for (int i = 0; i < P; ++i) angle(pos[0], i, cs[i], sn[i]);
+      for (int i = 0; i < P; ++i) angle<kFast>(a, pos[0], turns[i], cs[i], sn[i]);
     }
     for (int h = h0; h < h1; h += HB) {
       if (h != h0) load(h);
@@ -145,7 +164,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
       float c1[P], s1[P];
       if (pair) {
 #pragma unroll
-        for (int p = 0; p < P; ++p) angle(pos[i], p, c1[p], s1[p]);
+        for (int p = 0; p < P; ++p) angle<kFast>(a, pos[i], turns[p], c1[p], s1[p]);
       }
 #pragma unroll
       for (int k = 0; k < HB; ++k)
@@ -177,11 +196,67 @@ cudaError_t run_order(const RopeArgs& a, bool inter, cudaStream_t s) {
   return inter ? run<T, P, true>(a, s) : run<T, P, false>(a, s);
 }
 
-}  // namespace
+// dx = (dqk turned back) + dv; a.in is dqk, float32 and contiguous like dv.
+template <class T, int P, bool INTER>
+__global__ void __launch_bounds__(kThreads)
+rope_sum_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr int HB = 2;   // heads in flight, two float32 arrays each
+  stream_wait();
+  let_next_start();
+  const int tt = (int)a.fu.div(threadIdx.x), u = (int)threadIdx.x - tt * (int)a.fu.d;
+  const int t = blockIdx.x * a.tile + tt;
+  if (tt >= a.tile || t >= a.tokens) return;
+  const int h0 = blockIdx.y * a.heads, h1 = min(a.H, h0 + a.heads);
+  const bool pair = u < a.pair_units;
+  const int c = pair ? u * (INTER ? 2 * P : P) : a.rot + (u - a.pair_units) * 2 * P;
+  const int second = pair ? a.half : P;
+  const int b = (int)a.fl.div((uint32_t)t), l = t - b * a.L;
+  const int64_t from = b * a.si.b + l * a.si.l + c;
+  T* out = (T*)a.out + (b * a.so.b + l * a.so.l + c);
+  float cs[P], sn[P];
+  if (pair) {
+    const int64_t pos =
+        a.pos0 + (a.pos ? (int64_t)__ldg(a.pos + (int64_t)b * a.pos_batch * a.L + l) : (int64_t)l);
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      angle<sizeof(T) == 2>(a, pos, __ldg(a.turns + u * P + i), cs[i], sn[i]);
+  }
+  for (int h = h0; h < h1; h += HB) {
+    Pairs<float, P, INTER> g[HB], v[HB];
+#pragma unroll
+    for (int k = 0; k < HB; ++k)
+      if (h + k < h1) {
+        g[k].load((const float*)a.in + from + (h + k) * a.si.h, second);
+        v[k].load(a.add + from + (h + k) * a.si.h, second);
+      }
+#pragma unroll
+    for (int k = 0; k < HB; ++k)
+      if (h + k < h1) {
+        float p[P], q[P], vp[P], vq[P];
+        g[k].get(p, q);
+        v[k].get(vp, vq);
+        if (pair) Pairs<float, P, INTER>::turn_pairs(p, q, cs, sn);
+#pragma unroll
+        for (int i = 0; i < P; ++i) p[i] += vp[i], q[i] += vq[i];
+        Pairs<T, P, INTER> o;
+        o.set(p, q);
+        o.store(out + (h + k) * a.so.h, second);
+      }
+  }
+}
 
-cudaError_t launch_rope(const lsh_rope_problem& q, const lsh_strides& sin, const lsh_strides& sout,
-                        const void* in, const uint64_t* turns, const int32_t* pos, int64_t pos0,
-                        void* out, bool inverse, int vp, cudaStream_t s) {
+template <class T, int P>
+cudaError_t run_sum(const RopeArgs& a, bool inter, cudaStream_t s) {
+  note_launch();
+  return launch_overlapped(inter ? rope_sum_kernel<T, P, true> : rope_sum_kernel<T, P, false>,
+                           dim3((unsigned)((a.tokens + a.tile - 1) / a.tile),
+                                (unsigned)((a.H + a.heads - 1) / a.heads)),
+                           kThreads, 0, s, a);
+}
+
+RopeArgs rope_args(const lsh_rope_problem& q, const lsh_strides& sin, const lsh_strides& sout,
+                   const void* in, const uint64_t* turns, const int32_t* pos, int64_t pos0,
+                   void* out, bool inverse, int vp, int ahead) {
   RopeArgs a{};
   a.in = in, a.out = out, a.si = sin, a.so = sout;
   a.turns = turns, a.pos = pos, a.pos0 = pos0;
@@ -195,9 +270,34 @@ cudaError_t launch_rope(const lsh_rope_problem& q, const lsh_strides& sin, const
   a.tile = std::max(1, kThreads / units);
   // enough CTAs for the GPU before a thread walks more heads
   const int64_t ctas = ((int64_t)a.tokens + a.tile - 1) / a.tile;
-  const int64_t split = std::min<int64_t>((q.H + kAhead - 1) / kAhead,
+  const int64_t split = std::min<int64_t>((q.H + ahead - 1) / ahead,
                                           std::max<int64_t>(1, 148 * 8 / ctas));
   a.heads = (int)((q.H + split - 1) / split);
+  return a;
+}
+
+}  // namespace
+
+cudaError_t launch_rope_sum(const lsh_rope_problem& q, const lsh_strides& sx, const float* dqk,
+                            const float* dv, const uint64_t* turns, const int32_t* pos,
+                            int64_t pos0, void* dx, int vp, cudaStream_t s) {
+  const lsh_strides flat = {(int64_t)q.H * q.L * q.d, (int64_t)q.L * q.d, q.d};
+  RopeArgs a = rope_args(q, flat, sx, dqk, turns, pos, pos0, dx, true, vp, 2);
+  a.add = dv;
+  if (q.dtype == LSH_BF16) {
+    if (vp == 4) return run_sum<__nv_bfloat16, 4>(a, q.interleaved, s);
+    if (vp == 2) return run_sum<__nv_bfloat16, 2>(a, q.interleaved, s);
+    return run_sum<__nv_bfloat16, 1>(a, q.interleaved, s);
+  }
+  if (vp == 4) return run_sum<float, 4>(a, q.interleaved, s);
+  if (vp == 2) return run_sum<float, 2>(a, q.interleaved, s);
+  return run_sum<float, 1>(a, q.interleaved, s);
+}
+
+cudaError_t launch_rope(const lsh_rope_problem& q, const lsh_strides& sin, const lsh_strides& sout,
+                        const void* in, const uint64_t* turns, const int32_t* pos, int64_t pos0,
+                        void* out, bool inverse, int vp, cudaStream_t s) {
+  const RopeArgs a = rope_args(q, sin, sout, in, turns, pos, pos0, out, inverse, vp, kAhead);
   if (q.dtype == LSH_BF16) {
     if (vp == 8) return run<__nv_bfloat16, 8, false>(a, s);
     if (vp == 4) return run_order<__nv_bfloat16, 4>(a, q.interleaved, s);

@@ -42,5 +42,8 @@ cudaError_t launch_dropout(const lsh_dropout_problem& q, uint32_t t, float scale
 cudaError_t launch_rope(const lsh_rope_problem& q, const lsh_strides& sin, const lsh_strides& sout,
                         const void* in, const uint64_t* turns, const int32_t* pos, int64_t pos0,
                         void* out, bool inverse, int vp, cudaStream_t s);
+cudaError_t launch_rope_sum(const lsh_rope_problem& q, const lsh_strides& sx, const float* dqk,
+                            const float* dv, const uint64_t* turns, const int32_t* pos,
+                            int64_t pos0, void* dx, int vp, cudaStream_t s);
 
 }  // namespace lsh

@@ -268,12 +268,12 @@ lsh_status lsh_residual_bwd(const lsh_residual_problem* q, const void* dy, const
 }
 
 // Pairs of one access: the most that divides the pairs and the copied rest
-// and that pointers and strides allow (at most 16 bytes at once).
+// and that pointers and strides allow (at most `most` bytes at once).
 static int rope_pairs(const lsh_rope_problem* q, const lsh_strides& x, const lsh_strides& y,
-                      const void* in, const void* out) {
+                      const void* in, const void* out, int most = 16) {
   const int64_t es = (int64_t)esize(q->dtype);
   const int per = q->interleaved ? 2 : 1;
-  for (int vp = (int)(16 / es) / per; vp > 1; vp /= 2) {
+  for (int vp = (int)(most / es) / per; vp > 1; vp /= 2) {
     const int64_t n = vp * per;
     if ((q->rot / 2) % vp == 0 && (q->d - q->rot) % (2 * vp) == 0 && stride_multiple(x, n) &&
         stride_multiple(y, n) && is_aligned(in, n * es) && is_aligned(out, n * es))
@@ -282,15 +282,22 @@ static int rope_pairs(const lsh_rope_problem* q, const lsh_strides& x, const lsh
   return 1;
 }
 
-static lsh_status rope_run(const lsh_rope_problem* q, const void* in, const uint64_t* turns,
-                           const int32_t* pos, int64_t pos0, void* out, bool inverse,
-                           lsh_stream_t stream) {
+static lsh_status check_rope(const lsh_rope_problem* q, int least) {
   if (!q) return LSH_ERR_INVALID_ARG;
   lsh_status st = check_sizes(q->B, q->H, q->L, q->d, q->dtype);
   if (st != LSH_OK) return st;
-  if (q->rot < 2 || q->rot % 2 != 0 || q->rot > q->d || q->d % 2 != 0) return LSH_ERR_INVALID_ARG;
+  if (q->rot < least || q->rot % 2 != 0 || q->rot > q->d || q->d % 2 != 0)
+    return LSH_ERR_INVALID_ARG;
   if ((q->interleaved | 1) != 1 || (q->pos_batch | 1) != 1 || !std::isfinite(q->amp))
     return LSH_ERR_INVALID_ARG;
+  return LSH_OK;
+}
+
+static lsh_status rope_run(const lsh_rope_problem* q, const void* in, const uint64_t* turns,
+                           const int32_t* pos, int64_t pos0, void* out, bool inverse,
+                           lsh_stream_t stream) {
+  lsh_status st = check_rope(q, 2);
+  if (st != LSH_OK) return st;
   lsh_strides x, y;
   if (!resolve(q->B, q->H, q->L, q->d, q->x, &x) || !resolve(q->B, q->H, q->L, q->d, q->y, &y))
     return LSH_ERR_INVALID_ARG;
@@ -307,6 +314,27 @@ static lsh_status rope_run(const lsh_rope_problem* q, const void* in, const uint
 lsh_status lsh_rope_fwd(const lsh_rope_problem* q, const void* x, const uint64_t* turns,
                         const int32_t* pos, int64_t pos0, void* y, lsh_stream_t stream) {
   return rope_run(q, x, turns, pos, pos0, y, false, stream);
+}
+
+lsh_status lsh_rope_bwd_sum(const lsh_rope_problem* q, const float* dqk, const float* dv,
+                            const uint64_t* turns, const int32_t* pos, int64_t pos0, void* dx,
+                            lsh_stream_t stream) {
+  lsh_status st = check_rope(q, 0);
+  if (st != LSH_OK) return st;
+  lsh_strides x;
+  if (!resolve(q->B, q->H, q->L, q->d, q->x, &x)) return LSH_ERR_INVALID_ARG;
+  if (q->d > kRopeMaxHead) return LSH_ERR_UNSUPPORTED;
+  if ((int64_t)q->B * q->H * q->L == 0) return LSH_OK;
+  if (!dqk || !dv || !dx || (q->rot && !turns) || !is_aligned(dx, esize(q->dtype)) ||
+      !all_aligned({dqk, dv, pos}, 4) || !is_aligned(turns, 8))
+    return LSH_ERR_INVALID_ARG;
+  // the float32 side's accesses decide the width: four features at once
+  lsh_rope_problem f = *q;
+  f.dtype = LSH_F32;
+  lsh_strides c;
+  resolve(q->B, q->H, q->L, q->d, {0, 0, 0}, &c);
+  const int vp = std::min(rope_pairs(&f, c, c, dqk, dv), rope_pairs(q, x, x, dx, dx, 4 * (int)esize(q->dtype)));
+  return from_cuda(launch_rope_sum(*q, x, dqk, dv, turns, pos, pos0, dx, vp, (cudaStream_t)stream));
 }
 
 lsh_status lsh_rope_bwd(const lsh_rope_problem* q, const void* dy, const uint64_t* turns,

@@ -1,5 +1,6 @@
 """Torch-facing drivers of what surrounds a sublayer: norms, the residual add
-with its gate and dropout, dropout alone, and rotary positions.
+with its gate and dropout, dropout alone, rotary positions, and the reversible
+layer that joins them to the attention and the feed-forward.
 
 As in ``attention``: a driver is made for one fixed problem, owns its output
 buffers and workspaces (each call overwrites them; calls that overlap on the
@@ -18,6 +19,7 @@ device).
 """
 from __future__ import annotations
 
+import ctypes
 import math
 from typing import Optional, Sequence, Tuple, Union
 
@@ -52,6 +54,7 @@ class _Driver:
         if dev.type == "cuda" and dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
         self.device = dev
+        self._lib = _lib.lib()
         self._empty = self.B * self.H * self.L == 0
 
     def _strides(self, layout: Layout) -> Tuple[int, int, int, int]:
@@ -78,38 +81,48 @@ class _Driver:
             self.shape, strides)
 
     def _act(self, t, strides, name):
-        """Checks an activation."""
+        """Address of an activation that has the driver's shape, type, device
+        and the given strides. Decoding calls this for every token, so the
+        usual case is one expression."""
+        if t.dtype is self.tdtype and t.shape == self.shape and t.stride() == strides and \
+                t.device == self.device:
+            return t.data_ptr()
         if t.dtype is not self.tdtype or t.shape != self.shape or t.device != self.device:
             _refuse(type(self).__name__, f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, "
                                          f"expected {self.tdtype} {self.shape} on {self.device}")
-        if t.stride() != strides and not self._empty:
+        if not self._empty:
+            # strides of dimensions of one element say nothing
             for n, s, want in zip(self.shape, t.stride(), strides):
                 if n > 1 and s != want:
                     _refuse(type(self).__name__, f"{name}: strides {t.stride()}, "
                                                  f"the layout's are {strides}")
-        return t
+        return t.data_ptr()
 
     def _vec(self, t, shape, name, dtype=torch.float32):
-        if t is not None and (t.dtype is not dtype or t.shape != shape or
-                              t.device != self.device or not t.is_contiguous()):
-            _refuse(type(self).__name__, f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, "
-                                         f"expected contiguous {dtype} {shape} on {self.device}")
-        return t
-
-    def _stream(self, stream):
-        """The stream's handle; the driver's device must be the current one."""
-        if stream is None:
-            return torch._C._cuda_getCurrentRawStream(self.device.index)
-        return stream if isinstance(stream, int) else stream.cuda_stream
+        """Address of a contiguous parameter (None: none)."""
+        if t is None:
+            return None
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == self.device:
+            return t.data_ptr()
+        _refuse(type(self).__name__, f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, "
+                                     f"expected contiguous {dtype} {shape} on {self.device}")
 
     def _call(self, fn, *args):
-        if torch.cuda.current_device() != self.device.index:
-            with torch.cuda.device(self.device):
-                code = fn(*args)
+        """fn(*args, stream) with the driver's device current; a stream of None
+        is that device's current stream."""
+        here = torch._C._cuda_getDevice()
+        if here == self.device.index:
+            stream = args[-1]
+            if stream is None:
+                stream = torch._C._cuda_getCurrentRawStream(here)
+            elif not isinstance(stream, int):
+                stream = stream.cuda_stream
+            code = fn(*args[:-1], stream)
+            if code != 0:
+                raise _lib.LshError(code, type(self).__name__)
         else:
-            code = fn(*args)
-        if code != 0:
-            raise _lib.LshError(code, type(self).__name__)
+            with torch.cuda.device(self.device):
+                self._call(fn, *args)
 
     def _sized(self, n):
         if n == 0 and not self._empty:
@@ -121,7 +134,8 @@ class _Driver:
 
 
 def _seed(v, name):
-    v = int(v)
+    if v.__class__ is not int:
+        v = int(v)
     if not 0 <= v < 1 << 64:
         _refuse(name, "seed and offset are unsigned 64-bit numbers")
     return v
@@ -141,35 +155,34 @@ class Norm(_Driver):
         self.p = _lib.make_norm_problem(B, H, L, d, dtype, _KINDS[kind], eps, self.sx[:3],
                                         self.sh[:3])
         self.ws_bytes = self._sized(_lib.lsh_norm_bwd_workspace_size(self.p))
-        self.D = self.H * self.d
+        self._p = ctypes.byref(self.p)
+        self._D = (self.H * self.d,)
         self.h = self._buffer(self.sh)
         self.dx = self._buffer(self.sx)
-        self.dw = torch.empty(self.D, dtype=torch.float32, device=self.device)
+        self.dw = torch.empty(self._D, dtype=torch.float32, device=self.device)
         self.db = torch.empty_like(self.dw)
         self.ws = self._workspace(self.ws_bytes)
 
     def forward(self, x, w=None, b=None, out=None, stream=None):
-        h = self.h if out is None else self._act(out, self.sh, "out")
-        D = (self.D,)
-        self._call(_lib.lib().lsh_norm_fwd, self.p, self._act(x, self.sx, "x").data_ptr(),
-                   _lib._ptr(self._vec(w, D, "w")), _lib._ptr(self._vec(b, D, "b")),
-                   h.data_ptr(), self._stream(stream))
+        h = self.h if out is None else out
+        D = self._D
+        self._call(self._lib.lsh_norm_fwd, self._p, self._act(x, self.sx, "x"),
+                   self._vec(w, D, "w"), self._vec(b, D, "b"), self._act(h, self.sh, "out"), stream)
         return h
 
     def backward(self, x, dh, w=None, b=None, dres=None, out=None, stream=None):
         """(dx, dw, db): gradients of sum(h * dh), with ``dres`` (the gradient
         that reaches x past the norm) added to dx. dw and db are formed where w
         and b are given, else None."""
-        dx = self.dx if out is None else self._act(out, self.sx, "out")
-        D = (self.D,)
-        dw = None if self._vec(w, D, "w") is None else self.dw
-        db = None if self._vec(b, D, "b") is None else self.db
-        if dres is not None:
-            self._act(dres, self.sx, "dres")
-        self._call(_lib.lib().lsh_norm_bwd, self.p, self._act(x, self.sx, "x").data_ptr(),
-                   _lib._ptr(w), self._act(dh, self.sh, "dh").data_ptr(), _lib._ptr(dres),
-                   dx.data_ptr(), _lib._ptr(dw), _lib._ptr(db), self.ws.data_ptr(), self.ws_bytes,
-                   self._stream(stream))
+        dx = self.dx if out is None else out
+        D = self._D
+        self._vec(b, D, "b")
+        dw, db = None if w is None else self.dw, None if b is None else self.db
+        self._call(self._lib.lsh_norm_bwd, self._p, self._act(x, self.sx, "x"),
+                   self._vec(w, D, "w"), self._act(dh, self.sh, "dh"),
+                   None if dres is None else self._act(dres, self.sx, "dres"),
+                   self._act(dx, self.sx, "out"), _lib._ptr(dw), _lib._ptr(db),
+                   self.ws.data_ptr(), self.ws_bytes, stream)
         return dx, dw, db
 
 
@@ -193,21 +206,20 @@ class Dropout(_Driver):
         self.y = self._buffer(self.sy)
         self.dx = self._buffer(self.sx)
 
-    def _run(self, q, src, dst, seed, offset, counter, stream):
-        self._call(_lib.lib().lsh_dropout_fwd, q, src.data_ptr(), _seed(seed, "Dropout"),
-                   _seed(offset, "Dropout"),
-                   _lib._ptr(self._vec(counter, (1,), "counter", torch.int64)), dst.data_ptr(),
-                   self._stream(stream))
+    def _run(self, q, src, sx, dst, sy, seed, offset, counter, stream):
+        self._call(self._lib.lsh_dropout_fwd, ctypes.byref(q), self._act(src, sx, "input"),
+                   _seed(seed, "Dropout"), _seed(offset, "Dropout"),
+                   self._vec(counter, (1,), "counter", torch.int64), self._act(dst, sy, "out"),
+                   stream)
         return dst
 
     def forward(self, x, seed, offset=0, counter=None, out=None, stream=None):
-        y = self.y if out is None else self._act(out, self.sy, "out")
-        return self._run(self.p, self._act(x, self.sx, "x"), y, seed, offset, counter, stream)
+        return self._run(self.p, x, self.sx, self.y if out is None else out, self.sy, seed, offset,
+                         counter, stream)
 
     def backward(self, dy, seed, offset=0, counter=None, out=None, stream=None):
-        dx = self.dx if out is None else self._act(out, self.sx, "out")
-        return self._run(self.p_bwd, self._act(dy, self.sy, "dy"), dx, seed, offset, counter,
-                         stream)
+        return self._run(self.p_bwd, dy, self.sy, self.dx if out is None else out, self.sx, seed,
+                         offset, counter, stream)
 
 
 class Residual(_Driver):
@@ -237,8 +249,9 @@ class Residual(_Driver):
         # x from y: the same branch taken off, and the scale undone
         self.p_restore = problem(None, -alpha / beta, 1.0 / beta) if beta != 0 else None
         self.ws_bytes = self._sized(_lib.lsh_residual_bwd_workspace_size(self.p))
-        self.D = self.H * self.d
-        self.gate_shape = (self.B, self.D) if gate_batch else (self.D,)
+        self._p = ctypes.byref(self.p)
+        self._D = (self.H * self.d,)
+        self.gate_shape = (self.B, self._D[0]) if gate_batch else self._D
         f32 = dict(dtype=torch.float32, device=self.device)
         self.y = self._buffer(self.sx)
         self.h = self._buffer(self.sx) if norm else None
@@ -247,43 +260,41 @@ class Residual(_Driver):
         self.df = self._buffer(self.sf)
         self.dgate = self._buffer(self.sf) if gate == "sigmoid" else \
             torch.empty(self.gate_shape, **f32) if gate == "vector" else None
-        self.dw_post, self.db_post = ((torch.empty(self.D, **f32) for _ in range(2)) if post
+        self.dw_post, self.db_post = ((torch.empty(self._D, **f32) for _ in range(2)) if post
                                       else (None, None))
-        self.dw, self.db = ((torch.empty(self.D, **f32) for _ in range(2)) if norm
+        self.dw, self.db = ((torch.empty(self._D, **f32) for _ in range(2)) if norm
                             else (None, None))
         self.ws = self._workspace(self.ws_bytes)
 
     def _params(self, gate, w_post, b_post, w, b):
-        if (gate is None) != (self.gate is None):
-            _refuse("Residual", f"gate is {self.gate!r}")
-        if gate is not None:
-            if self.gate == "sigmoid":
-                self._act(gate, self.sf, "gate")
-            else:
-                self._vec(gate, self.gate_shape, "gate")
+        """Addresses of the gate and the parameters."""
+        if gate is None:
+            if self.gate is not None:
+                _refuse("Residual", f"gate is {self.gate!r}")
+        elif self.gate == "vector":
+            gate = self._vec(gate, self.gate_shape, "gate")
+        elif self.gate == "sigmoid":
+            gate = self._act(gate, self.sf, "gate")
+        else:
+            _refuse("Residual", "made without a gate")
         if not self.post and (w_post is not None or b_post is not None):
             _refuse("Residual", "w_post, b_post without a norm of f")
         if not self.norm and (w is not None or b is not None):
             _refuse("Residual", "w, b without a norm of y")
-        D = (self.D,)
-        for t, name in ((w_post, "w_post"), (b_post, "b_post"), (w, "w"), (b, "b")):
-            if t is not None:
-                self._vec(t, D, name)
-
-    def _join(self, q, x, f, gate, w_post, b_post, w, b, seed, offset, counter, y, h, stream):
-        ptr = _lib._ptr
-        self._call(_lib.lib().lsh_residual_fwd, q, x.data_ptr(), f.data_ptr(), ptr(gate),
-                   ptr(w_post), ptr(b_post), ptr(w), ptr(b), _seed(seed, "Residual"),
-                   _seed(offset, "Residual"), ptr(self._vec(counter, (1,), "counter", torch.int64)),
-                   y.data_ptr(), ptr(h), self._stream(stream))
+        D, vec = self._D, self._vec
+        return (gate, vec(w_post, D, "w_post"), vec(b_post, D, "b_post"), vec(w, D, "w"),
+                vec(b, D, "b"))
 
     def forward(self, x, f, gate=None, w_post=None, b_post=None, w=None, b=None, seed=0, offset=0,
                 counter=None, stream=None):
         """(y, h); h is None without a norm."""
-        self._params(gate, w_post, b_post, w, b)
-        self._join(self.p, self._act(x, self.sx, "x"), self._act(f, self.sf, "f"), gate, w_post,
-                   b_post, w, b, seed, offset, counter, self.y, self.h, stream)
-        return self.y, self.h
+        y, h = self.y, self.h
+        self._call(self._lib.lsh_residual_fwd, self._p, self._act(x, self.sx, "x"),
+                   self._act(f, self.sf, "f"), *self._params(gate, w_post, b_post, w, b),
+                   _seed(seed, "Residual"), _seed(offset, "Residual"),
+                   self._vec(counter, (1,), "counter", torch.int64), y.data_ptr(),
+                   None if h is None else h.data_ptr(), stream)
+        return y, h
 
     def restore(self, y, f, gate=None, w_post=None, b_post=None, seed=0, offset=0, counter=None,
                 stream=None):
@@ -291,9 +302,11 @@ class Residual(_Driver):
         from its output, with the same branch, seed and offset."""
         if self.p_restore is None:
             _refuse("Residual", "beta = 0 cannot be undone")
-        self._params(gate, w_post, b_post, None, None)
-        self._join(self.p_restore, self._act(y, self.sx, "y"), self._act(f, self.sf, "f"), gate,
-                   w_post, b_post, None, None, seed, offset, counter, self.x, None, stream)
+        self._call(self._lib.lsh_residual_fwd, ctypes.byref(self.p_restore),
+                   self._act(y, self.sx, "y"), self._act(f, self.sf, "f"),
+                   *self._params(gate, w_post, b_post, None, None), _seed(seed, "Residual"),
+                   _seed(offset, "Residual"), self._vec(counter, (1,), "counter", torch.int64),
+                   self.x.data_ptr(), None, stream)
         return self.x
 
     def backward(self, dy, f, y=None, dh=None, gate=None, w_post=None, b_post=None, w=None, b=None,
@@ -302,26 +315,24 @@ class Residual(_Driver):
         sum(h * dh). y (forward's) and dh are needed with a norm, where dy may
         be None (zeros). Parameter gradients are formed for the parameters
         given, else None."""
-        self._params(gate, w_post, b_post, w, b)
+        p_gate, p_wp, p_bp, p_w, _ = self._params(gate, w_post, b_post, w, b)
+        p_y = p_dh = None
         if self.norm:
-            self._act(y, self.sx, "y")
-            self._act(dh, self.sx, "dh")
-        elif dh is not None:
-            _refuse("Residual", "dh without a norm of y")
-        if dy is not None:
-            self._act(dy, self.sx, "dy")
+            if y is None or dh is None:
+                _refuse("Residual", "the backward of a norm needs y and dh")
+            p_y, p_dh = self._act(y, self.sx, "y"), self._act(dh, self.sx, "dh")
+        elif dh is not None or dy is None:
+            _refuse("Residual", "without a norm of y the gradient is dy alone")
         dw_post = None if w_post is None else self.dw_post
         db_post = None if b_post is None else self.db_post
-        dw = None if w is None else self.dw
-        db = None if b is None else self.db
+        dw, db = None if w is None else self.dw, None if b is None else self.db
         ptr = _lib._ptr
-        self._call(_lib.lib().lsh_residual_bwd, self.p, ptr(dy), ptr(dh),
-                   ptr(y) if self.norm else None, self._act(f, self.sf, "f").data_ptr(), ptr(gate),
-                   ptr(w_post), ptr(b_post), ptr(w), _seed(seed, "Residual"),
-                   _seed(offset, "Residual"), ptr(self._vec(counter, (1,), "counter", torch.int64)),
+        self._call(self._lib.lsh_residual_bwd, self._p,
+                   None if dy is None else self._act(dy, self.sx, "dy"), p_dh, p_y,
+                   self._act(f, self.sf, "f"), p_gate, p_wp, p_bp, p_w, _seed(seed, "Residual"),
+                   _seed(offset, "Residual"), self._vec(counter, (1,), "counter", torch.int64),
                    self.dx.data_ptr(), self.df.data_ptr(), ptr(self.dgate), ptr(dw_post),
-                   ptr(db_post), ptr(dw), ptr(db), self.ws.data_ptr(), self.ws_bytes,
-                   self._stream(stream))
+                   ptr(db_post), ptr(dw), ptr(db), self.ws.data_ptr(), self.ws_bytes, stream)
         return self.dx, self.df, self.dgate, dw_post, db_post, dw, db
 
 
@@ -396,27 +407,195 @@ class Rotary(_Driver):
         self.sx, self.sy = self._strides(x_layout), self._strides(y_layout)
         self.p = [_lib.make_rope_problem(B, H, L, d, dtype, self.rot, interleaved, pb, self.amp,
                                          self.sx[:3], self.sy[:3]) for pb in (0, 1)]
+        self._p = [ctypes.byref(q) for q in self.p]
+        self._turns = self.turns.data_ptr()   # the driver's own table
         self.y = self._buffer(self.sy)
         self.dx = self._buffer(self.sx)
 
-    def _run(self, fn, src, dst, pos, pos0, stream):
-        q = self.p[0]
+    def _run(self, fn, src, ss, dst, sd, pos, pos0, stream):
+        q = self._p[0]
         if pos is not None:
             if pos.dim() == 2:
-                q = self.p[1]
-                self._vec(pos, (self.B, self.L), "pos", torch.int32)
+                q = self._p[1]
+                pos = self._vec(pos, (self.B, self.L), "pos", torch.int32)
             else:
-                self._vec(pos, (self.L,), "pos", torch.int32)
-        self._call(fn, q, src.data_ptr(), self.turns.data_ptr(), _lib._ptr(pos), int(pos0),
-                   dst.data_ptr(), self._stream(stream))
+                pos = self._vec(pos, (self.L,), "pos", torch.int32)
+        self._call(fn, q, self._act(src, ss, "input"), self._turns, pos, int(pos0),
+                   self._act(dst, sd, "out"), stream)
         return dst
 
     def forward(self, x, pos=None, pos0=0, out=None, stream=None):
         """Position of token (b, l): pos0 + l, or pos0 + pos[l] / pos[b, l] (int32)."""
-        y = self.y if out is None else self._act(out, self.sy, "out")
-        return self._run(_lib.lib().lsh_rope_fwd, self._act(x, self.sx, "x"), y, pos, pos0, stream)
+        return self._run(self._lib.lsh_rope_fwd, x, self.sx, self.y if out is None else out,
+                         self.sy, pos, pos0, stream)
 
     def backward(self, dy, pos=None, pos0=0, out=None, stream=None):
-        dx = self.dx if out is None else self._act(out, self.sx, "out")
-        return self._run(_lib.lib().lsh_rope_bwd, self._act(dy, self.sy, "dy"), dx, pos, pos0,
-                         stream)
+        return self._run(self._lib.lsh_rope_bwd, dy, self.sy, self.dx if out is None else out,
+                         self.sx, pos, pos0, stream)
+
+    def backward_sum(self, dqk, dv, pos=None, pos0=0, out=None, stream=None):
+        """dx = (backward of dqk) + dv for an activation that fed the attention
+        both turned and as it is; dqk, dv: the attention's float32 gradients,
+        contiguous."""
+        dx = self.dx if out is None else out
+        f32 = torch.float32
+        q, addr = self._p[0], None
+        if pos is not None:
+            two = pos.dim() == 2
+            q = self._p[1] if two else q
+            addr = self._vec(pos, (self.B, self.L) if two else (self.L,), "pos", torch.int32)
+        self._call(self._lib.lsh_rope_bwd_sum, q, self._vec(dqk, self.shape, "dqk", f32),
+                   self._vec(dv, self.shape, "dv", f32), self._turns, addr, int(pos0),
+                   self._act(dx, self.sx, "out"), stream)
+        return dx
+
+
+class ReversibleLayer(_Driver):
+    """One reversible layer with what a trained one has around its sublayers:
+
+      y1 = x1 + alpha drop(gate1 post1(F(n))),  n = norm1(x2)
+      y2 = x2 + alpha drop(gate2 post2(G(m))),  m = norm2(y1)
+
+    F is LSH attention with qk = rope(n), v = n (without rotary positions qk =
+    n); G the chunked feed-forward. The backward rebuilds x1 and x2 from y1 and
+    y2: the dropout masks are recomputed from (seed, offset, position), so
+    nothing of the forward is kept but the sort permutation.
+
+    bf16, contiguous [B, H, L, 64]. norm: "layer" or "rms"; post: None or one
+    of them; gate: False or True (a learned float32 vector [64 H] for each
+    sublayer); rot: rotated features of a head (0: no positions). Parameters
+    are a dict: norm1_w, norm2_w (and norm1_b, norm2_b for "layer"), post1_w,
+    post2_w (and post1_b, post2_b), gate1, gate2, as far as the layer has them,
+    all float32 [64 H], and the feed-forward's W1 [64 H, d_ff], W2 [d_ff, 64 H]
+    (bf16), b1, b2 (float32).
+
+    Both sublayers draw from (seed, offset + counter): the attention's mask at
+    that offset, the feed-forward's at offset + 2^63; give every layer and step
+    its own seed or offset (below 2^63)."""
+
+    def __init__(self, B, H, L, n_buckets, n_rounds, chunk, causal, d_ff, ff_chunk, norm="layer",
+                 post=None, gate=False, p=0.0, alpha=1.0, rot=64, interleaved=False, base=10000.0,
+                 scaling=None, eps=1e-5, slice0=0, device="cuda"):
+        from .attention import LSHAttention
+        super().__init__(B, H, L, 64, "bf16", device)
+        if norm not in ("layer", "rms"):
+            _refuse("ReversibleLayer", f"norm {norm!r}")
+        kw = dict(device=self.device)
+        self.norm, self.post, self.gate = norm, post, bool(gate)
+        self.attn = LSHAttention(B, H, L, n_buckets, n_rounds, chunk, causal, **kw)
+        self.f = _lib.make_ff_problem(B, H, L, d_ff, ff_chunk)
+        self.ff_ws_bytes = self._sized(_lib.lsh_ff_workspace_size(self.f))
+        self.ff_ws = self._workspace(self.ff_ws_bytes)
+        self.norm1 = Norm(B, H, L, norm, eps, **kw)
+        self.norm2 = Norm(B, H, L, norm, eps, **kw)
+        join = dict(post=post, gate="vector" if gate else None, p=p, alpha=alpha, eps=eps,
+                    slice0=slice0, **kw)
+        self.join1 = Residual(B, H, L, norm=norm, **join)
+        self.join2 = Residual(B, H, L, **join)
+        self.rope = Rotary(B, H, L, rot, interleaved, base, scaling, **kw) if rot else None
+        if not rot:
+            self._sum = _lib.make_rope_problem(B, H, L, 64, "bf16", 0, False, False, 1.0)
+        self.D, self.d_ff = 64 * self.H, int(d_ff)
+        f32 = dict(dtype=torch.float32, device=self.device)
+        act = lambda: self._buffer(self._strides("head"))
+        self.g, self.dm, self.dn, self.dx2 = act(), act(), act(), act()
+        self.dW1 = torch.empty((self.D, self.d_ff), **f32)
+        self.db1 = torch.empty((self.d_ff,), **f32)
+        self.dW2 = torch.empty((self.d_ff, self.D), **f32)
+        self.db2 = torch.empty((self.D,), **f32)
+
+    def _check(self, w):
+        want = {"W1", "b1", "W2", "b2"}
+        for i in "12":
+            want |= {f"norm{i}_w"} | ({f"norm{i}_b"} if self.norm == "layer" else set())
+            if self.post:
+                want |= {f"post{i}_w"} | ({f"post{i}_b"} if self.post == "layer" else set())
+            if self.gate:
+                want.add(f"gate{i}")
+        if set(w) != want:
+            _refuse("ReversibleLayer", f"parameters {sorted(w)}, expected {sorted(want)}")
+        bf16 = torch.bfloat16
+        self._vec(w["W1"], (self.D, self.d_ff), "W1", bf16)
+        self._vec(w["W2"], (self.d_ff, self.D), "W2", bf16)
+        self._vec(w["b1"], (self.d_ff,), "b1")
+        self._vec(w["b2"], (self.D,), "b2")
+
+    def _offsets(self, offset):
+        if not 0 <= int(offset) < 1 << 63:
+            _refuse("ReversibleLayer", "offset is below 2^63")
+        return int(offset), int(offset) + (1 << 63)
+
+    @staticmethod
+    def _branch(w, i):
+        """The parameters that sublayer i's join takes."""
+        return dict(gate=w.get(f"gate{i}"), w_post=w.get(f"post{i}_w"),
+                    b_post=w.get(f"post{i}_b"))
+
+    def _attend(self, x2, w, pos0, stream, R=None):
+        """F(norm1(x2)); sorts by R's buckets, or keeps the permutation."""
+        n = self.norm1.forward(x2, w["norm1_w"], w.get("norm1_b"), stream=stream)
+        q = n if self.rope is None else self.rope.forward(n, pos0=pos0, stream=stream)
+        if R is not None:
+            self.attn.hash(q, R, stream)
+            self.attn.sort(None, stream)
+        return n, q, self.attn.attend(q, n, None, stream)[0]
+
+    def _feed(self, m, w, stream):
+        self._call(self._lib.lsh_ff_fwd, ctypes.byref(self.f), m.data_ptr(), w["W1"].data_ptr(),
+                   w["b1"].data_ptr(), w["W2"].data_ptr(), w["b2"].data_ptr(), None,
+                   self.g.data_ptr(), self.ff_ws.data_ptr(), self.ff_ws_bytes, stream)
+        return self.g
+
+    def forward(self, x1, x2, R, w, seed=0, offset=0, counter=None, pos0=0, stream=None):
+        """(y1, y2); R [n_rounds, 64, n_buckets / 2] bf16. Token l of every
+        sequence has position pos0 + l."""
+        self._check(w)
+        o1, o2 = self._offsets(offset)
+        head = self._strides("head")
+        self._act(x1, head, "x1"), self._act(x2, head, "x2")
+        p = self.attn.p
+        self._vec(R, (p.n_rounds, 64, p.n_buckets // 2), "R", torch.bfloat16)
+        _, _, f = self._attend(x2, w, pos0, stream, R)
+        rng = dict(seed=seed, counter=counter, stream=stream)
+        y1, m = self.join1.forward(x1, f, **self._branch(w, 1), w=w["norm2_w"], b=w.get("norm2_b"),
+                                   offset=o1, **rng)
+        y2, _ = self.join2.forward(x2, self._feed(m, w, stream), **self._branch(w, 2), offset=o2,
+                                   **rng)
+        return y1, y2
+
+    def backward(self, y1, y2, dy1, dy2, w, seed=0, offset=0, counter=None, pos0=0, stream=None):
+        """(x1, x2, dx1, dx2, grads): the inputs rebuilt from the outputs and
+        the gradients of sum(y1 dy1) + sum(y2 dy2); grads is a dict like w, all
+        float32. Uses the permutation of the last forward of this driver."""
+        self._check(w)
+        o1, o2 = self._offsets(offset)
+        rng = dict(seed=seed, counter=counter, stream=stream)
+        b1, b2 = self._branch(w, 1), self._branch(w, 2)
+        # feed-forward half: x2 = y2 - branch(G(m)), then G's gradients
+        m = self.norm2.forward(y1, w["norm2_w"], w.get("norm2_b"), stream=stream)
+        g = self._feed(m, w, stream)
+        x2 = self.join2.restore(y2, g, **b2, offset=o2, **rng)
+        dx2, dg, *d2 = self.join2.backward(dy2, g, **b2, offset=o2, **rng)
+        self._call(self._lib.lsh_ff_bwd, ctypes.byref(self.f), m.data_ptr(), w["W1"].data_ptr(),
+                   w["b1"].data_ptr(), w["W2"].data_ptr(), w["b2"].data_ptr(), dg.data_ptr(), None,
+                   None, None, self.dm.data_ptr(), self.dW1.data_ptr(), self.db1.data_ptr(),
+                   self.dW2.data_ptr(), self.db2.data_ptr(), self.ff_ws.data_ptr(),
+                   self.ff_ws_bytes, stream)
+        # attention half: F(norm1(x2)) again, x1 = y1 - branch(F), F's gradients
+        n, q, f = self._attend(x2, w, pos0, stream)
+        x1 = self.join1.restore(y1, f, **b1, offset=o1, **rng)
+        dx1, df, *d1 = self.join1.backward(dy1, f, y=y1, dh=self.dm, **b1, w=w["norm2_w"],
+                                           b=w.get("norm2_b"), offset=o1, **rng)
+        dqk, dv = self.attn.backward(q, n, df, None, stream)
+        if self.rope is not None:
+            dn = self.rope.backward_sum(dqk, dv, pos0=pos0, out=self.dn, stream=stream)
+        else:
+            dn = self.dn
+            self._call(self._lib.lsh_rope_bwd_sum, ctypes.byref(self._sum), dqk.data_ptr(),
+                       dv.data_ptr(), None, None, 0, dn.data_ptr(), stream)
+        _, dw, db = self.norm1.backward(x2, dn, w["norm1_w"], w.get("norm1_b"), dres=dx2,
+                                        out=self.dx2, stream=stream)
+        grads = dict(W1=self.dW1, b1=self.db1, W2=self.dW2, b2=self.db2, norm1_w=dw, norm1_b=db,
+                     gate1=d1[0], post1_w=d1[1], post1_b=d1[2], norm2_w=d1[3], norm2_b=d1[4],
+                     gate2=d2[0], post2_w=d2[1], post2_b=d2[2])
+        return x1, x2, dx1, self.dx2, {k: v for k, v in grads.items() if v is not None}

@@ -400,6 +400,16 @@ lsh_status lsh_rope_fwd(const lsh_rope_problem* q, const void* x, const uint64_t
                         const int32_t* pos, int64_t pos0, void* y, lsh_stream_t stream);
 lsh_status lsh_rope_bwd(const lsh_rope_problem* q, const void* dy, const uint64_t* turns,
                         const int32_t* pos, int64_t pos0, void* dx, lsh_stream_t stream);
+/*
+ * lsh_rope_bwd_sum: the gradient of an activation n that fed the attention
+ *   both turned (qk = rope(n)) and as it is (v = n): dx = (lsh_rope_bwd of dqk)
+ *   + dv, from lsh_attn_bwd's float32 gradients, contiguous [B, H, L, d],
+ *   rounded once to `dtype`. dx has the strides x; y is not used. rot may be
+ *   0 (turns may then be NULL): dx = dqk + dv.
+ */
+lsh_status lsh_rope_bwd_sum(const lsh_rope_problem* q, const float* dqk, const float* dv,
+                            const uint64_t* turns, const int32_t* pos, int64_t pos0, void* dx,
+                            lsh_stream_t stream);
 
 /*
  * lsh_sort_noalloc — lsh_sort without a caller workspace. The reference pages

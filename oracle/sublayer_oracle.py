@@ -8,6 +8,9 @@ from __future__ import annotations
 
 import numpy as np
 
+from oracle import lsh_oracle as lsh
+from oracle import rev_ff_oracle as ff
+
 M32 = 0xFFFFFFFF
 
 
@@ -122,3 +125,71 @@ def rope(x, freqs, pos, rot, interleaved=False, amp=1.0, inverse=False):
     y[..., lo] = x[..., lo] * c - x[..., hi] * s
     y[..., hi] = x[..., hi] * c + x[..., lo] * s
     return y
+
+
+# --------------------------------------------------------------------------
+# The reversible layer: y1 = x1 + a drop(g1 post1(F(n))), n = norm1(x2), F =
+# attention with qk = rope(n), v = n; y2 = x2 + a drop(g2 post2(G(m))), m =
+# norm2(y1). `c` holds the constants: norm, post, gate, alpha, eps, freqs (None:
+# no positions), rot, interleaved, amp, pos, chunk, causal, scale, and the two
+# sublayers' dropout factors fac1, fac2. `w` holds the parameters by name.
+# --------------------------------------------------------------------------
+
+def _turn(x, c, inverse=False):
+    if c["freqs"] is None:
+        return x
+    return rope(x, c["freqs"], c["pos"], c["rot"], c["interleaved"], c["amp"], inverse)
+
+
+def _join(w, i, c):
+    return dict(post=c["post"], gate=w.get(f"gate{i}"), kind="vector" if c["gate"] else None,
+                alpha=c["alpha"], eps=c["eps"], w_post=w.get(f"post{i}_w"),
+                factor=c[f"fac{i}"])
+
+
+def _feed(m, w, B, H, L):
+    return ff.tokens_to_heads(ff.ff_forward(ff.heads_to_tokens(m), w["W1"], w["b1"], w["W2"],
+                                            w["b2"]), B, H, L)
+
+
+def _norm(x, w, i, c):
+    return norm_forward(x, c["norm"], c["eps"], w[f"norm{i}_w"], w.get(f"norm{i}_b"))
+
+
+def layer_forward(x1, x2, perm, w, c):
+    """(y1, y2)"""
+    B, H, L, _ = x1.shape
+    n = _norm(x2, w, 1, c)
+    f, _ = lsh.forward(_turn(n, c), n, perm, c["chunk"], c["causal"], c["scale"])
+    y1 = residual_forward(x1, f, **_join(w, 1, c), b_post=w.get("post1_b"))
+    g = _feed(_norm(y1, w, 2, c), w, B, H, L)
+    return y1, residual_forward(x2, g, **_join(w, 2, c), b_post=w.get("post2_b"))
+
+
+def layer_backward(y1, y2, dy1, dy2, perm, w, c):
+    """(x1, x2, dx1, dx2, grads) from the outputs."""
+    B, H, L, _ = y1.shape
+    zero = np.zeros_like(y1)
+    m = _norm(y1, w, 2, c)
+    g = _feed(m, w, B, H, L)
+    j2 = _join(w, 2, c)
+    x2 = y2 - residual_forward(zero, g, **j2, b_post=w.get("post2_b"))
+    r2 = residual_backward(dy2, None, None, g, **j2, b_post=w.get("post2_b"))
+    dm, dW1, db1, dW2, db2 = ff.ff_backward(ff.heads_to_tokens(m), w["W1"], w["b1"], w["W2"],
+                                            w["b2"], ff.heads_to_tokens(r2["df"]))
+    n = _norm(x2, w, 1, c)
+    q = _turn(n, c)
+    f, lse = lsh.forward(q, n, perm, c["chunk"], c["causal"], c["scale"])
+    j1 = _join(w, 1, c)
+    x1 = y1 - residual_forward(zero, f, **j1, b_post=w.get("post1_b"))
+    r1 = residual_backward(dy1, ff.tokens_to_heads(dm, B, H, L), y1, f, norm=c["norm"],
+                           w=w["norm2_w"], **j1, b_post=w.get("post1_b"))
+    dqk, dv = lsh.backward(q, n, perm, c["chunk"], c["causal"], c["scale"], f, lse, r1["df"])
+    dx2, dw, db = norm_backward(x2, c["norm"], c["eps"], w["norm1_w"], _turn(dqk, c, True) + dv,
+                                r2["dx"])
+    out = dict(W1=dW1, b1=db1, W2=dW2, b2=db2, norm1_w=dw, norm1_b=db, norm2_w=r1["dw"],
+               norm2_b=r1["db"])
+    for i, r in ((1, r1), (2, r2)):
+        out.update({f"gate{i}": r.get("dgate"), f"post{i}_w": r.get("dw_post"),
+                    f"post{i}_b": r.get("db_post")})
+    return x1, x2, r1["dx"], dx2, {k: out[k] for k in w}

@@ -555,3 +555,243 @@ def test_backward_stays_inside_its_workspace(H, d, dtype, tokens):
     _lib.lsh_residual_bwd(q, dy, dh, x, f, gate, w, w, w, 1, 0, None, dx, df,
                           torch.empty_like(gate), grads[1], grads[2], grads[4], None, buf, size)
     assert (buf[size:] == 77).all()
+
+
+@pytest.mark.parametrize("B,H,L,d,dtype,rot,inter,yl", [
+    (2, 3, 33, 64, "bf16", 64, False, "head"), (1, 8, 65, 64, "bf16", 32, True, "token"),
+    (2, 1, 9, 64, "f32", 64, True, "head"), (1, 2, 17, 64, "bf16", 0, False, "head"),
+    (1, 3, 5, 10, "f32", 6, False, "odd"), (1, 2, 7, 64, "f32", 20, False, "slice")])
+def test_rope_backward_sum(B, H, L, d, dtype, rot, inter, yl):
+    from efficient_transformer_lsh_b200 import _lib
+    from efficient_transformer_lsh_b200 import sublayer as sl
+    torch = _torch()
+    g = np.random.default_rng(L + rot)
+    shape = (B, H, L, d)
+    lay, strides = _layouts(yl, *shape)
+    dqk, dqk64 = _f32(g.standard_normal(shape))
+    dv, dv64 = _f32(g.standard_normal(shape))
+    pos = torch.arange(L, dtype=torch.int32, device="cuda") * 3
+    td = torch.bfloat16 if dtype == "bf16" else torch.float32
+    k = 22 if dtype == "bf16" else 9        # test_rope's, and the sum's rounding
+    if rot:
+        r = sl.Rotary(B, H, L, rot, inter, dtype=dtype, d=d, x_layout=lay)
+        got = r.backward_sum(dqk, dv, pos, 5)
+        freqs, amp = sl.rope_frequencies(rot)
+        turned = orc.rope(dqk64, freqs, 5 + 3 * np.arange(L), rot, inter, amp, True)
+        pair = _pair_sum(np.abs(dqk64), rot, inter)
+    else:
+        q = _lib.make_rope_problem(B, H, L, d, dtype, 0, False, False, 1.0)
+        got = torch.empty(shape, dtype=td, device="cuda")
+        _lib.lsh_rope_bwd_sum(q, dqk, dv, None, None, 0, got)
+        turned, pair = dqk64, np.abs(dqk64)
+    _close(got, turned + dv64, dtype, pair + np.abs(dv64), k)
+
+
+def _layer(post, gate, norm, rot, p, causal, seed, B=2, H=2, L=256, dff=256):
+    from efficient_transformer_lsh_b200 import sublayer as sl
+    torch = _torch()
+    g = np.random.default_rng(seed)
+    nb, nr = 16, 2
+    run = sl.ReversibleLayer(B, H, L, nb, nr, 64, causal, dff, 128, norm=norm, post=post, gate=gate,
+                             p=p, alpha=0.5, rot=rot)
+    D, shape = 64 * H, (B, H, L, 64)
+    w, w64 = {}, {}
+
+    def par(name, a, dtype="f32"):
+        w[name], w64[name] = _put(a, dtype) if dtype == "bf16" else _f32(a)
+
+    par("W1", g.standard_normal((D, dff)) / np.sqrt(D), "bf16")
+    par("W2", g.standard_normal((dff, D)) / np.sqrt(dff), "bf16")
+    par("b1", 0.1 * g.standard_normal(dff))
+    par("b2", 0.1 * g.standard_normal(D))
+    for i in "12":
+        par(f"norm{i}_w", 1 + 0.2 * g.standard_normal(D))
+        if norm == "layer":
+            par(f"norm{i}_b", 0.1 * g.standard_normal(D))
+        if post:
+            par(f"post{i}_w", 1 + 0.2 * g.standard_normal(D))
+        if post == "layer":
+            par(f"post{i}_b", 0.1 * g.standard_normal(D))
+        if gate:
+            par(f"gate{i}", 0.8 + 0.2 * g.standard_normal(D))
+    acts = [_put(g.standard_normal(shape), "bf16") for _ in range(4)]
+    R = _put(g.standard_normal((nr, 64, nb // 2)), "bf16")[0]
+    return run, w, w64, acts, R
+
+
+@pytest.mark.parametrize("post,gate,norm,rot,p,causal", [
+    (None, False, "layer", 64, 0.0, True), ("layer", True, "layer", 32, 0.1, True),
+    ("rms", False, "rms", 0, 0.25, False), (None, True, "rms", 64, 0.1, False)])
+def test_reversible_layer_stage_by_stage(post, gate, norm, rot, p, causal):
+    """Every stage of the layer against the oracle's formula of what the GPU
+    gave it (attention: the path's 2e-2; products: the rounding of the hidden
+    layer; the rest as above), then the whole against the oracle."""
+    from efficient_transformer_lsh_b200 import _lib
+    from efficient_transformer_lsh_b200 import sublayer as sl
+    from oracle import lsh_oracle as lsh
+    from oracle import rev_ff_oracle as ff
+    torch = _torch()
+    run, w, w64, acts, R = _layer(post, gate, norm, rot, p, causal, 5)
+    (x1, x1_), (x2, x2_), (dy1, dy1_), (dy2, dy2_) = acts
+    B, H, L, _ = run.shape
+    D, seed, off = 64 * H, 99, 7
+    num = lambda t: t.double().cpu().numpy()
+    tok = ff.heads_to_tokens
+    kind = "vector" if gate else None
+    eps = 1e-5
+    fac = [orc.dropout_factor(run.shape, p, seed, o) for o in (off, off + (1 << 63))]
+
+    y1, y2 = run.forward(x1, x2, R, w, seed=seed, offset=off, pos0=3)
+    assert _lib.lsh_device_status() == 0
+    n, f, m, g = (num(t) for t in (run.norm1.h, run.attn.out, run.join1.h, run.g))
+    y1_, y2_ = num(y1), num(y2)
+    perm = run.attn.perm.cpu().numpy().astype(np.int64)
+    nm = lambda x, i: orc.norm_forward(x, norm, eps, w64[f"norm{i}_w"], w64.get(f"norm{i}_b"))
+    mag = lambda x, i: _norm_mag(x, norm, eps, w64[f"norm{i}_w"], w64.get(f"norm{i}_b"))
+    _close(run.norm1.h, nm(x2_, 1), "bf16", mag(x2_, 1))
+    freqs, amp = sl.rope_frequencies(rot) if rot else (None, 1.0)
+    turn = lambda a, inv=False: a if not rot else orc.rope(a, freqs, 3 + np.arange(L), rot, False,
+                                                           amp, inv)
+    q = num(run.rope.y) if rot else n
+    if rot:
+        _close(run.rope.y, turn(n), "bf16", _pair_sum(np.abs(n), rot, False), 22)
+    F, LSE = lsh.forward(q, n, perm, 64, causal, 0.125)
+    assert np.abs(f - F).max() <= 2e-2
+
+    def join(x, f, i):
+        wp, bp = w64.get(f"post{i}_w"), w64.get(f"post{i}_b")
+        gt = w64.get(f"gate{i}")
+        y = orc.residual_forward(x, f, post, gt, kind, 0.5, 1.0, eps, wp, bp, fac[i - 1])
+        um = _norm_mag(f, post, eps, wp, bp) if post else np.abs(f)
+        return y, np.abs(x) + fac[i - 1] * (np.abs(orc._p(gt, f.shape)) if gate else 1.0) * um
+
+    _close(y1, *_swap(join(x1_, f, 1)))
+    _close(run.join1.h, nm(y1_, 2), "bf16", mag(y1_, 2))
+    W = [w64[k] for k in ("W1", "b1", "W2", "b2")]
+    hid = np.maximum(tok(m) @ W[0] + W[1], 0)
+    want = ff.ff_forward(tok(m), *W)
+    assert (np.abs(tok(g) - want) <= 2.0 ** -8 * (np.abs(want) + hid @ np.abs(W[2])) + 1e-3).all()
+    _close(y2, *_swap(join(x2_, g, 2)))
+
+    keep_g, keep_m, keep_f = (t.clone() for t in (run.g, run.join1.h, run.attn.out))
+    rx1, rx2, dx1, dx2, grads = run.backward(y1, y2, dy1, dy2, w, seed=seed, offset=off, pos0=3)
+    assert _lib.lsh_device_status() == 0
+    # the recomputation saw the forward's m, mask and G, bit for bit
+    assert torch.equal(run.norm2.h, keep_m) and torch.equal(run.g, keep_g)
+    half = 2.0 ** -8
+    assert (np.abs(num(rx2) - x2_) <= half * (np.abs(y2_) + np.abs(num(rx2))) + 1e-4).all()
+    # x1 = y1 - branch(F(rebuilt x2)): F moves by what x2 moved
+    f2 = num(run.attn.out)
+    back, bm = join(np.zeros_like(y1_), f2, 1)
+    _close(rx1, y1_ - back, "bf16", np.abs(y1_) + bm)
+    rx2_ = num(rx2)
+    n2, q2 = num(run.norm1.h), num(run.rope.y) if rot else num(run.norm1.h)
+
+    def jb(dy, dh, y, f, i, nrm):
+        return orc.residual_backward(dy, dh, y, f, post, nrm, w64.get(f"gate{i}"), kind, 0.5, 1.0,
+                                     eps, w64.get(f"post{i}_w"), w64.get(f"post{i}_b"),
+                                     w64["norm2_w"] if nrm else None, fac[i - 1])
+
+    def near(got, want, rel):
+        """2-norm of the difference over that of the result."""
+        a = num(got)
+        assert np.linalg.norm(a - want) <= rel * np.linalg.norm(want) + 1e-6, \
+            np.linalg.norm(a - want) / np.linalg.norm(want)
+
+    # one bf16 rounding a value: 2^-8 of it; sums in float32 nearer
+    r2 = jb(dy2_, None, None, g, 2, None)
+    near(run.join2.df, r2["df"], half)
+    dm, dW1, db1, dW2, db2 = ff.ff_backward(tok(m), *W, tok(num(run.join2.df)))
+    # the hidden layer and its gradient are rounded to bf16 (an element at the
+    # kink may fall on the other side: its value is within a rounding of zero)
+    near(run.dm, ff.tokens_to_heads(dm, B, H, L), 3 * half)
+    for k, v in (("W1", dW1), ("b1", db1), ("W2", dW2), ("b2", db2)):
+        near(grads[k], v, 2 * half)
+    r1 = jb(dy1_, num(run.dm), y1_, f2, 1, norm)
+    near(dx1, r1["dx"], half)
+    near(run.join1.df, r1["df"], half)
+    for key, name in (("dgate", "gate"), ("dw_post", "post{}_w"), ("db_post", "post{}_b")):
+        for i, r in ((1, r1), (2, r2)):
+            k = name.format(i) if "{" in name else f"{name}{i}"
+            if k in grads:
+                near(grads[k], r[key], 2e-5)
+    near(grads["norm2_w"], r1["dw"], 2e-5)
+    F2, LSE2 = lsh.forward(q2, n2, perm, 64, causal, 0.125)
+    dqk, dv = lsh.backward(q2, n2, perm, 64, causal, 0.125, F2, LSE2, num(run.join1.df))
+    assert np.abs(num(run.attn.dqk) - dqk).max() <= 2e-2
+    assert np.abs(num(run.attn.dv) - dv).max() <= 2e-2
+    near(run.dn, turn(num(run.attn.dqk), True) + num(run.attn.dv), half)
+    ex, ew, eb = orc.norm_backward(rx2_, norm, eps, w64["norm1_w"], num(run.dn), num(run.join2.dx))
+    near(dx2, ex, half)
+    near(grads["norm1_w"], ew, 2e-5)
+    assert set(grads) == set(w)
+    # the whole, from the outputs: about thirteen roundings of 2^-8 on the way,
+    # none amplified by more than 2 in these well-conditioned layers
+    c = dict(norm=norm, post=post, gate=gate, alpha=0.5, eps=eps, freqs=freqs, rot=rot,
+             interleaved=False, amp=amp, pos=3 + np.arange(L), chunk=64, causal=causal, scale=0.125,
+             fac1=fac[0], fac2=fac[1])
+    _, _, wx1, wx2, wg = orc.layer_backward(y1_, y2_, dy1_, dy2_, perm, w64, c)
+    near(dx1, wx1, 0.1)
+    near(dx2, wx2, 0.1)
+    for k in w:
+        near(grads[k], wg[k], 0.1)
+
+
+def _swap(pair):
+    """(value, magnitude) as _close's (want, dtype, magnitude)."""
+    return pair[0], "bf16", pair[1]
+
+
+def test_reversible_layer_captured_and_replayed():
+    """Forward and backward in one graph; each replay sees the counter's new
+    masks, and the rebuilt inputs are those of an eager layer's."""
+    from efficient_transformer_lsh_b200 import _lib
+    torch = _torch()
+    run, w, _, acts, R = _layer("rms", True, "layer", 64, 0.2, True, 11)
+    other = _layer("rms", True, "layer", 64, 0.2, True, 11)[0]
+    x1, x2, dy1, dy2 = (a[0] for a in acts)
+    counter = torch.zeros(1, dtype=torch.int64, device="cuda")
+
+    def step(r):
+        y1, y2 = r.forward(x1, x2, R, w, seed=3, counter=counter)
+        out = r.backward(y1, y2, dy1, dy2, w, seed=3, counter=counter)
+        return [y1, y2, *out[:4], *(out[4][k] for k in sorted(out[4]))]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(run)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            outs = step(run)
+    side.synchronize()
+    seen = []
+    for i in range(3):
+        counter.fill_(i)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        want = step(other)
+        torch.cuda.synchronize()
+        # the weight gradients of the products are checked by norm: their K
+        # splits are added in a fixed order, so they are equal too
+        for a, b in zip(outs, want):
+            assert torch.equal(a, b)
+        seen.append(outs[0].clone())
+        assert (outs[2].float() - x1.float()).abs().max() < 0.1
+    assert not torch.equal(seen[0], seen[1]) and not torch.equal(seen[1], seen[2])
+    assert _lib.lsh_device_status() == 0
+
+
+def test_reversible_layer_refuses():
+    from efficient_transformer_lsh_b200 import _lib
+    run, w, _, acts, R = _layer(None, False, "layer", 64, 0.1, True, 1)
+    x1, x2 = acts[0][0], acts[1][0]
+    for bad in ({k: v for k, v in w.items() if k != "norm1_b"}, {**w, "gate1": w["b2"]},
+                {**w, "W1": w["W1"].float()}, {**w, "norm1_w": w["b1"][:64]}):
+        with pytest.raises(_lib.LshError):
+            run.forward(x1, x2, R, bad)
+    with pytest.raises(_lib.LshError):
+        run.forward(x1, x2, R[:1], w)
+    with pytest.raises(_lib.LshError):
+        run.forward(x1, x2, R, w, offset=1 << 63)

@@ -132,3 +132,50 @@ def test_frequency_tables():
             # 53 bits of f and of 2 pi: three roundings of 2^-53 each, and 2^-64 a position
             err = (got - pos * v / (2 * math.pi) + 0.5) % 1.0 - 0.5
             assert abs(err) < abs(pos) * (v * 4 * 2.0 ** -53 + 2.0 ** -63) + 2.0 ** -52
+
+
+@pytest.mark.parametrize("post,gate,rot", [(None, False, 0), ("rms", True, 8), ("layer", True, 64)])
+def test_reversible_layer_inverts_and_differentiates(post, gate, rot):
+    """The layer's backward rebuilds its inputs, and its gradients are the
+    differences of its forward (the permutation held fixed)."""
+    from oracle import lsh_oracle as lsh
+    g = np.random.default_rng(7)
+    B, H, L, D, dff = 1, 2, 8, 128, 12
+    shape = (B, H, L, 64)
+    x1, x2, dy1, dy2 = (g.standard_normal(shape) for _ in range(4))
+    w = dict(W1=g.standard_normal((D, dff)) / 11, b1=0.1 * g.standard_normal(dff),
+             W2=g.standard_normal((dff, D)) / 4, b2=0.1 * g.standard_normal(D))
+    for i in (1, 2):
+        w[f"norm{i}_w"], w[f"norm{i}_b"] = 1 + 0.2 * g.standard_normal(D), g.standard_normal(D)
+        if post:
+            w[f"post{i}_w"] = 1 + 0.2 * g.standard_normal(D)
+        if post == "layer":
+            w[f"post{i}_b"] = g.standard_normal(D)
+        if gate:
+            w[f"gate{i}"] = 0.7 + 0.2 * g.standard_normal(D)
+    c = dict(norm="layer", post=post, gate=gate, alpha=0.7, eps=1e-4, rot=rot, interleaved=True,
+             amp=1.1, pos=np.arange(L) + 3, chunk=4, causal=True, scale=0.125,
+             freqs=[10.0 ** (-i / 8) for i in range(rot // 2)] if rot else None,
+             fac1=orc.dropout_factor(shape, 0.2, 5, 1), fac2=orc.dropout_factor(shape, 0.2, 5, 2))
+    perm = np.stack([[g.permutation(L) for _ in range(2)] for _ in range(B * H)]).reshape(B, H, 2, L)
+    y1, y2 = orc.layer_forward(x1, x2, perm, w, c)
+    rx1, rx2, dx1, dx2, grads = orc.layer_backward(y1, y2, dy1, dy2, perm, w, c)
+    assert np.abs(rx1 - x1).max() < 1e-11 and np.abs(rx2 - x2).max() < 1e-11
+
+    def value(x1, x2, w):
+        a, b = orc.layer_forward(x1, x2, perm, w, c)
+        return (a * dy1).sum() + (b * dy2).sum()
+
+    def diff(fn, a, i, step=1e-5):
+        p, q = a.copy(), a.copy()
+        p.flat[i] += step
+        q.flat[i] -= step
+        return (fn(p) - fn(q)) / (2 * step)
+
+    for i in range(3, x1.size, 131):
+        assert abs(diff(lambda a: value(a, x2, w), x1, i) - dx1.flat[i]) < 1e-6
+        assert abs(diff(lambda a: value(x1, a, w), x2, i) - dx2.flat[i]) < 1e-6
+    for k in w:
+        for i in range(1, w[k].size, max(2, w[k].size // 3)):
+            d = diff(lambda a: value(x1, x2, {**w, k: a}), w[k], i)
+            assert abs(d - grads[k].flat[i]) < 1e-6 * max(1.0, abs(d)), k

@@ -233,3 +233,18 @@ def test_problem_structs_match_the_header():
                  (_lib.lsh_dropout_problem, 80), (_lib.lsh_residual_problem, 112),
                  (_lib.lsh_rope_problem, 88)):
         assert ctypes.sizeof(s) == n, s
+
+
+def test_rope_backward_sum_refuses(L):
+    ok = [FAKE, FAKE, FAKE, None, 0, FAKE, None]
+    for kw, code in ((dict(rot=3), 1), (dict(rot=-2), 1), (dict(rot=66), 1), (dict(B=-1), 1),
+                     (dict(x=(1, 2, 3)), 1), (dict(d=514), 2)):
+        assert L.lsh_rope_bwd_sum(_rope(**kw), *ok) == code
+    for i in (0, 1, 2, 5):                 # dqk, dv, turns, dx
+        bad = list(ok)
+        bad[i] = None
+        assert L.lsh_rope_bwd_sum(_rope(), *bad) == 1
+    bad = list(ok)
+    bad[0] = FAKE + 2
+    assert L.lsh_rope_bwd_sum(_rope(), *bad) == 1
+    assert L.lsh_rope_bwd_sum(_rope(B=0), None, None, None, None, 0, None, None) == 0
