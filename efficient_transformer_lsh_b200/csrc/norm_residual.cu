@@ -16,7 +16,7 @@ SubShape sub_shape(const SubCall& c, const SubSize& z) {
   s.wide = c.wide;
   for (const lsh_strides* t : {&c.sx, &c.sf, &c.sh})
     if ((c.H - 1) * t->h + c.d > (int64_t)INT32_MAX) s.wide = false;
-  int ctas;
+  int ctas, fixed;
   for (;;) {
     const int per = s.wide ? z.per : kNarrowPer, threads = s.wide ? z.threads : kNarrowThreads;
     s.tok = s.wide ? z.tok : 1;
@@ -32,23 +32,29 @@ SubShape sub_shape(const SubCall& c, const SubSize& z) {
       s.team = 32;
     }
     // Teams of several warps: two tokens at a time halve the barriers, which
-    // pays where a branch makes many (4 x 4096 x 4096, everything on: 238 us
-    // against 307), but a norm alone gains more from twice the warps (196
-    // against 247); 512 threads of two tokens do not fit the register file.
+    // pays where a branch makes many (4 x 4096 tokens of 4096 features: 238
+    // us against 307), but a norm alone gains more from twice the warps (4 x
+    // 8192 of 4096: 196 against 247); 512 threads of two tokens do not fit the
+    // register file.
     if (z.backward && (s.team > 256 || (s.team > 32 && !c.branch))) s.tok = 1;
     s.teams = std::max(1, threads / s.team);
     s.threads = s.teams * s.team;
     // threads resident on an SM, by the registers of each form
     int room = 512;
-    if (z.backward && s.wide && s.team > 32 && z.tok > 1) room = s.tok > 1 ? 256 : 512;
+    if (z.backward && s.wide && s.team > 32 && z.tok > 1) room = s.tok == 1 ? 512 : kBwdMultiRoom;
     else if (s.wide) room = z.ctas * threads;
     ctas = std::max(1, room / s.threads);
-    const int fixed = z.vecs * per * 4 * s.team + (s.team > 32 ? s.teams * 64 * kMaxWarps : 0);
+    fixed = z.vecs * per * 4 * s.team + (s.team > 32 ? s.teams * 64 * kMaxWarps : 0);
     s.stages = 1;
     s.smem = fixed;
     if (s.wide) {
       const int stage = z.tensors * s.tok * (s.team > 32 ? s.threads : threads) * per * esize;
-      while (ctas > 1 && fixed + 2 * stage > kSmemPerSm / ctas - 1024) --ctas;
+      // two stages before more CTAs, unless that many CTAs have no second
+      // round to copy ahead for
+      const int64_t all = ((int64_t)s.tokens + s.teams * s.tok - 1) / (s.teams * s.tok) * s.groups;
+      while (ctas > 1 && fixed + stage > kSmemPerSm / ctas - 1024) --ctas;
+      if (all > kSms * ctas)
+        while (ctas > 1 && fixed + 2 * stage > kSmemPerSm / ctas - 1024) --ctas;
       if (fixed + stage > kSmemPerSm / ctas - 1024) {
         s.wide = false;
         continue;
@@ -60,6 +66,13 @@ SubShape sub_shape(const SubCall& c, const SubSize& z) {
   }
   const int64_t rows = ((int64_t)s.tokens + s.teams * s.tok - 1) / (s.teams * s.tok);
   s.parts = (int)std::min<int64_t>(rows, max_parts(std::min(kSms * ctas, kMaxParts), s.groups));
+  // no more stages than rounds
+  if (s.wide && s.parts > 0) {
+    const int rounds = (int)std::min<int64_t>(kMaxStages, (rows + s.parts - 1) / s.parts);
+    const int stage = (s.smem - fixed) / s.stages;
+    s.stages = std::min(s.stages, rounds);
+    s.smem = fixed + s.stages * stage;
+  }
   return s;
 }
 
@@ -108,38 +121,50 @@ struct FinalArgs {
   float *dgate, *dwp, *dbp, *dw, *db;
 };
 
-// Adds the CTAs' rows, in order. Block (x, y): 32 features, y = 0 the norm's
-// pair, y = 1 the branch's; warp w of 32 adds rows w, w + 32, ... of a group,
-// then warp 0 adds the warps' sums.
-__global__ void __launch_bounds__(1024) sub_final_kernel(const FinalArgs a) {
-  __shared__ float buf[2][32][33];
+// Adds the CTAs' rows, in a fixed order. Block (x, y): 8 features (one sector),
+// y = 0 the norm's pair, y = 1 the branch's; 64 threads a feature add rows i,
+// i + 64, ... of a group, all loads in flight, then a warp's four, then the
+// warps in order. (32 features and 32 threads each: 9.2 us for 444 rows of 512
+// features, the latency of two rounds of loads on 16 SMs.)
+constexpr int kFinalCols = 8, kFinalRows = 64;
+__global__ void __launch_bounds__(kFinalCols* kFinalRows)
+sub_final_kernel(const __grid_constant__ FinalArgs a) {
+  __shared__ float buf[2][kFinalCols * kFinalRows / 32][kFinalCols];
   stream_wait();
   let_next_start();
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
+  const int col = threadIdx.x % kFinalCols, i = threadIdx.x / kFinalCols, w = threadIdx.x >> 5;
+  const int c = blockIdx.x * kFinalCols + col;
   const bool on = c < a.D;
   const bool branch = a.norm ? blockIdx.y == 1 : true;
   const int v0 = branch && a.norm ? 2 : 0;
-  float t1 = 0.f, t0 = 0.f;   // warp 0: totals over the groups
+  const int64_t row = (int64_t)a.vecs * a.D;
+  float t1 = 0.f, t0 = 0.f;   // the first threads: totals over the groups
   for (int g = 0; g < a.groups; ++g) {
     float s1 = 0.f, s0 = 0.f;
     if (on) {
-      const float* r = a.part + ((int64_t)g * a.parts * a.vecs + v0) * a.D + c;
-      const int64_t row = (int64_t)a.vecs * a.D;
+      const float* r = a.part + (int64_t)g * a.parts * row + v0 * a.D + c;
 #pragma unroll 8
-      for (int p = w; p < a.parts; p += 32) {
+      for (int p = i; p < a.parts; p += kFinalRows) {
         s1 += __ldcg(r + p * row);
         s0 += __ldcg(r + p * row + a.D);
       }
     }
-    buf[0][w][lane] = s1;
-    buf[1][w][lane] = s0;
+#pragma unroll
+    for (int o = kFinalCols; o < 32; o <<= 1) {
+      s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+      s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+    }
+    if ((threadIdx.x & 31) < kFinalCols) {
+      buf[0][w][col] = s1;
+      buf[1][w][col] = s0;
+    }
     __syncthreads();
-    if (w == 0 && on) {
+    if (i == 0 && on) {
       s1 = s0 = 0.f;
-      for (int k = 0; k < 32; ++k) {
-        s1 += buf[0][k][lane];
-        s0 += buf[1][k][lane];
+#pragma unroll
+      for (int k = 0; k < kFinalCols * kFinalRows / 32; ++k) {
+        s1 += buf[0][k][col];
+        s0 += buf[1][k][col];
       }
       if (branch) {
         const float gate = a.gv ? a.gv[(a.gate_batch ? (int64_t)g * a.D : 0) + c] : 1.f;
@@ -155,7 +180,7 @@ __global__ void __launch_bounds__(1024) sub_final_kernel(const FinalArgs a) {
     }
     __syncthreads();
   }
-  if (w == 0 && on) {
+  if (i == 0 && on) {
     float* o1 = branch ? a.dwp : a.dw;
     float* o0 = branch ? a.dbp : a.db;
     if (o1) o1[c] = t1;
@@ -216,8 +241,9 @@ cudaError_t launch_sub_bwd(const SubCall& c, void* ws, cudaStream_t st) {
   f.dgate = c.dgate, f.dwp = c.dwp, f.dbp = c.dbp, f.dw = c.dw, f.db = c.db;
   note_launch();
   return launch_overlapped(sub_final_kernel,
-                           dim3((unsigned)((a.D + 31) / 32), (unsigned)(f.norm + f.branch)), 1024,
-                           0, st, f);
+                           dim3((unsigned)((a.D + kFinalCols - 1) / kFinalCols),
+                                (unsigned)(f.norm + f.branch)),
+                           kFinalCols * kFinalRows, 0, st, f);
 }
 
 }  // namespace lsh

@@ -118,8 +118,10 @@ __device__ __forceinline__ void scale_all(f2 (&v)[N], float m) {
 }
 
 // g = 1 / (1 + exp(-z)); slope = g (1 - g), without the cancellation in 1 - g.
+// The approximate exponential and quotient are right to a few units of 2^-24
+// of the result (the exponent is at most 0, the quotient's divisor in [1, 2]).
 __device__ __forceinline__ float sigmoid(float z, float& slope) {
-  const float e = expf(-fabsf(z)), i = 1.f / (1.f + e);
+  const float e = __expf(-fabsf(z)), i = __fdividef(1.f, 1.f + e);
   slope = e * i * i;
   return z >= 0.f ? i : e * i;
 }
@@ -174,6 +176,7 @@ struct Place {
   static constexpr bool kRing = V > 1;
   static constexpr int kSlots = PER * (int)sizeof(T) / 16;   // 16 bytes each
   static constexpr int kKeep = kRing ? NV : 1;
+  static constexpr uint32_t kAll = (uint32_t)((1ull << NV) - 1);
   const SubArgs& a;
   int group, part, team_id, lane;   // lane: thread of the team
   int ox[kKeep], of[kKeep], oh[kKeep];   // a vector's place in a token, by strides
@@ -403,9 +406,8 @@ struct Place {
   // Parameters sit in shared memory as [vector][PER / 4][team] groups of four.
   __device__ __forceinline__ void stage_param(int vec, const float* p, const float* q,
                                               bool zero = false) const {
-    if (team_id != 0) return;
-#pragma unroll
-    for (int j = 0; j < PER / 4; ++j) {
+    // the teams of the CTA share the groups out
+    for (int j = team_id; j < PER / 4; j += a.teams) {
       const float4 u = param4(p, q, zero, j);
       sts16(par + (vec * (PER / 4) + j) * team() * 16,
             make_uint4(__float_as_uint(u.x), __float_as_uint(u.y), __float_as_uint(u.z),
@@ -485,6 +487,8 @@ struct Place {
     }
     scale_all(v, m);
   }
+  // Features of the thread that exist.
+  __device__ __forceinline__ float count() const { return (float)(__popc(on_bits) * V); }
   // v - m on the features that exist, 0 elsewhere
   __device__ __forceinline__ void center(f2 (&v)[P], float m) const {
     if constexpr (kRing) {
@@ -542,20 +546,35 @@ cudaError_t with_team(int team, F f) {
 // Features a thread, tokens a team, threads of a CTA of several teams and CTAs
 // of an SM, for the wide kernels. Forward: 32 features, so that a warp takes
 // two tokens of 512. Backward: the four sums of parameter gradients already
-// take four registers a feature, so 16 features, and two tokens at a time in
-// bf16; one in float32, where a token is twice the bytes, and with a sigmoid
-// gate, whose registers for two would spill (64K x 512 features: 207 us
-// against 155).
+// take four registers a feature, so 16 features, and a few warps with all the
+// registers they can use, rather than more that spill (64K tokens of 512
+// features with everything on: bf16 with two tokens at a time 100 us at 255
+// registers, 2 x 128 threads an SM, 104 at 168, 3 x 128; float32 with one token
+// 73 for 32K at 255 registers against 103 at 128, 2 x 256). A sigmoid gate's
+// kernel takes one token and 168 registers (114 us; 143 at 128, 127 at 255).
 constexpr int kFwdPer = 32, kFwdThreads = 256, kFwdCtas = 2, kFwdNormCtas = 3;
 constexpr int kBwdPer = 16;
 constexpr int kNarrowThreads = 256;
 template <class T, bool SIG>
 struct BwdSize {
-  static constexpr bool kTwo = sizeof(T) == 2 && !SIG;
-  static constexpr int kTok = kTwo ? 2 : 1;
-  static constexpr int kThreads = kTwo ? 128 : 256;
-  static constexpr int kCtas = kTwo ? 3 : 2;
+  static constexpr int kTok = sizeof(T) == 2 && !SIG ? 2 : 1;
+  static constexpr int kThreads = 128;
+  static constexpr int kCtas = SIG ? 3 : 2;
 };
+
+// Largest CTA and residency that a backward kernel is compiled for: a team of
+// up to a warp in CTAs of BwdSize; several warps with one token as many as 512
+// threads; with two tokens 256, 255 registers a thread.
+constexpr int kBwdMultiRoom = 256;
+template <class T, int V, int TEAM, int TOK, bool SIG>
+constexpr int bwd_threads() {
+  return TEAM != 0 ? (V == 1 ? kNarrowThreads : BwdSize<T, SIG>::kThreads)
+                   : TOK == 1 ? 32 * kMaxWarps : 256;
+}
+template <class T, int V, int TEAM, int TOK, bool SIG>
+constexpr int bwd_ctas() {
+  return TEAM != 0 ? (V == 1 ? 2 : BwdSize<T, SIG>::kCtas) : 1;
+}
 
 template <class T>
 cudaError_t sub_fwd_type(const SubCall& c, const SubArgs& a, const SubShape& s, cudaStream_t st);

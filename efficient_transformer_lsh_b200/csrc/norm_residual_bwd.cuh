@@ -48,10 +48,8 @@ __device__ __forceinline__ void write_part(const At& at, const f2 (&s)[At::P], f
 // Parameters, in order: W, P1 = gate w_post (a sigmoid gate is not in it), P0
 // = b_post (sigmoid gates only).
 template <class T, int V, int PER, int TEAM, int TOK, bool BRANCH, bool NORM, bool POST, bool SIG>
-__global__ void __launch_bounds__(TEAM != 0  ? (V == 1 ? kNarrowThreads : BwdSize<T, SIG>::kThreads)
-                                  : TOK == 1 ? 32 * kMaxWarps
-                                             : 256,
-                                  TEAM != 0 ? (V == 1 ? 2 : BwdSize<T, SIG>::kCtas) : 1)
+__global__ void __launch_bounds__(bwd_threads<T, V, TEAM, TOK, SIG>(),
+                                  bwd_ctas<T, V, TEAM, TOK, SIG>())
 sub_bwd_kernel(const __grid_constant__ SubArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   using At = Place<T, V, PER, TEAM, TOK, V == 1 ? kNarrowThreads : BwdSize<T, SIG>::kThreads>;
@@ -63,17 +61,14 @@ sub_bwd_kernel(const __grid_constant__ SubArgs a) {
   constexpr bool post = BRANCH && POST, sig = BRANCH && SIG;
   const float* gv = a.gv ? a.gv + (int64_t)at.group * (a.gate_batch ? a.D : 0) : nullptr;
   const bool has1 = BRANCH && (a.wp || gv), has0 = sig && a.bp;
-  if (NORM) at.stage_param(0, a.w, nullptr);
-  if (has1) at.stage_param(kP1, a.wp, gv);
-  if (has0) at.stage_param(kP0, a.bp, nullptr);
   // the ring's tensors: y dh, dy, f, z
   const int i_dy = NORM ? 2 : 0, i_f = i_dy + (a.dy ? 1 : 0), i_z = i_f + 1;
   const int tensors = i_f + BRANCH + sig;
-  at.clear(at.ring, a.stages * tensors * TOK);
-  __syncthreads();
+  if (at.on_bits != At::kAll) at.clear(at.ring, a.stages * tensors * TOK);
   const uint64_t offset = a.offset + (a.counter ? __ldg(a.counter) : 0);
   const int step = at.step(), rounds = at.rounds();
   const uint32_t one = at.one(), token_bytes = tensors * one, stage_bytes = TOK * token_bytes;
+  const float own = at.count();
   const bool lf = post && a.post == LSH_NORM_LAYER, ly = NORM && a.norm == LSH_NORM_LAYER;
   f2 sa[P], sb[P], s1[P], s0[P];
 #pragma unroll
@@ -114,7 +109,12 @@ sub_bwd_kernel(const __grid_constant__ SubArgs a) {
       cp_commit();
     }
   };
+  // the first tokens are on the way while the parameters are staged
   for (int i = 1; i < a.stages; ++i) copy();
+  if (NORM) at.stage_param(0, a.w, nullptr);
+  if (has1) at.stage_param(kP1, a.wp, gv);
+  if (has0) at.stage_param(kP0, a.bp, nullptr);
+  __syncthreads();
   uint32_t st = at.ring;
   int t = at.first();
   for (int n = 0; n < rounds; ++n, t += step) {
@@ -139,6 +139,9 @@ sub_bwd_kernel(const __grid_constant__ SubArgs a) {
     f2 q[TOK][P];     // T, then q, then du
     f2 hat[TOK][P];   // y - mean, then f - mean, then fhat
     float r_f[TOK], mean_f[TOK];
+    // a thread's own mean and squared deviations of f: those of the row follow
+    // from them (Chan, Golub and LeVeque 1979) without another look at f
+    float own_mean[TOK], own_sq[TOK];
     if constexpr (NORM) {
 #pragma unroll
       for (int j = 0; j < TOK; ++j) {
@@ -154,6 +157,9 @@ sub_bwd_kernel(const __grid_constant__ SubArgs a) {
           if (lf) {
             get_f(a.f, i_f, j, q[j]);
             s[2 * j + 1] = sum_all(q[j]);
+            own_mean[j] = at.on_bits ? s[2 * j + 1] / own : 0.f;
+            at.center(q[j], own_mean[j]);
+            own_sq[j] = dot_all(q[j], q[j]);
           }
         }
         at.team_sum(s);
@@ -167,9 +173,11 @@ sub_bwd_kernel(const __grid_constant__ SubArgs a) {
 #pragma unroll
       for (int j = 0; j < TOK; ++j) {
         s[4 * j + 3] = 0.f;
-        if (post) {
+        if (lf) {
+          const float d = own_mean[j] - mean_f[j];
+          s[4 * j + 3] = fmaf(own * d, d, own_sq[j]);
+        } else if (post) {
           get_f(a.f, i_f, j, q[j]);
-          if (lf) at.center(q[j], mean_f[j]);
           s[4 * j + 3] = dot_all(q[j], q[j]);
         }
         s[4 * j] = dot_all(hat[j], hat[j]);

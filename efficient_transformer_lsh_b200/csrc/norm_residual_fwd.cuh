@@ -27,13 +27,8 @@ sub_fwd_kernel(const __grid_constant__ SubArgs a) {
   const float* gv = a.gv ? a.gv + (int64_t)at.group * (a.gate_batch ? a.D : 0) : nullptr;
   const bool has1 = BRANCH && (a.wp || gv), has0 = BRANCH && a.bp;
   constexpr int kW = 0, kP1 = 1, kB = BRANCH ? 2 : 1, kP0 = 3;
-  if (norm && (a.w || a.b)) at.stage_param(kW, a.w, nullptr);
-  if (has1 || has0) at.stage_param(kP1, a.wp, gv);
-  if (norm && a.b) at.stage_param(kB, a.b, nullptr);
-  if (has0) at.stage_param(kP0, a.bp, gv);
   const int tensors = 1 + BRANCH + sig;
-  at.clear(at.ring, a.stages * tensors * TOK);
-  __syncthreads();
+  if (at.on_bits != At::kAll) at.clear(at.ring, a.stages * tensors * TOK);
   const uint64_t offset = a.offset + (a.counter ? __ldg(a.counter) : 0);
   const int step = at.step(), rounds = at.rounds();
   const uint32_t one = at.one(), token_bytes = tensors * one, stage_bytes = TOK * token_bytes;
@@ -65,11 +60,16 @@ sub_fwd_kernel(const __grid_constant__ SubArgs a) {
       cp_commit();
     }
   };
-  for (int i = 1; i < a.stages; ++i) copy();
+  // the first tokens are on the way while the parameters are staged
+  for (int i = 0; i < a.stages; ++i) copy();
+  if (norm && (a.w || a.b)) at.stage_param(kW, a.w, nullptr);
+  if (has1 || has0) at.stage_param(kP1, a.wp, gv);
+  if (norm && a.b) at.stage_param(kB, a.b, nullptr);
+  if (has0) at.stage_param(kP0, a.bp, gv);
+  __syncthreads();
   uint32_t st = at.ring;
   int t = at.first();
   for (int n = 0; n < rounds; ++n, t += step) {
-    copy();
     if constexpr (At::kRing) cp_wait_for(a.stages - 1);
     int b[TOK], l[TOK];
     bool live[TOK];
@@ -145,6 +145,7 @@ sub_fwd_kernel(const __grid_constant__ SubArgs a) {
     }
     st += stage_bytes;
     if (st == at.ring + a.stages * stage_bytes) st = at.ring;
+    copy();
   }
   if constexpr (At::kRing) cp_wait<0>();
 }
