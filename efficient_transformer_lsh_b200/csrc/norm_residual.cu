@@ -18,8 +18,11 @@ SubShape sub_shape(const SubCall& c, const SubSize& z) {
     if ((c.H - 1) * t->h + c.d > (int64_t)INT32_MAX) s.wide = false;
   int ctas, fixed;
   for (;;) {
-    const int per = s.wide ? z.per : kNarrowPer, threads = s.wide ? z.threads : kNarrowThreads;
-    s.tok = s.wide ? z.tok : 1;
+    const bool wide_norm = s.wide && z.backward && !c.branch && D > 32 * kBwdPer;
+    const int per = !s.wide ? kNarrowPer : wide_norm ? kBwdWidePer : z.per;
+    const int threads = s.wide ? z.threads : kNarrowThreads;
+    s.per = per;
+    s.tok = s.wide && !wide_norm ? z.tok : 1;
     // threads of a token: a power of two up to a warp, then whole warps
     s.team = (D + per - 1) / per;
     if (s.team > 32) {
@@ -31,18 +34,14 @@ SubShape sub_shape(const SubCall& c, const SubSize& z) {
     } else {
       s.team = 32;
     }
-    // Teams of several warps: two tokens at a time halve the barriers, which
-    // pays where a branch makes many (4 x 4096 tokens of 4096 features: 238
-    // us against 307), but a norm alone gains more from twice the warps (4 x
-    // 8192 of 4096: 196 against 247); 512 threads of two tokens do not fit the
-    // register file.
-    if (z.backward && (s.team > 256 || (s.team > 32 && !c.branch))) s.tok = 1;
+    // 512 threads of two tokens each do not fit the register file
+    if (s.team > 256) s.tok = 1;
     s.teams = std::max(1, threads / s.team);
     s.threads = s.teams * s.team;
     // threads resident on an SM, by the registers of each form
     int room = 512;
-    if (z.backward && s.wide && s.team > 32 && z.tok > 1) room = s.tok == 1 ? 512 : kBwdMultiRoom;
-    else if (s.wide) room = z.ctas * threads;
+    if (wide_norm || (z.backward && s.wide && s.team > 32 && s.tok > 1)) room = kBwdRoom;
+    else if (s.wide && (!z.backward || s.team <= 32)) room = z.ctas * threads;
     ctas = std::max(1, room / s.threads);
     fixed = z.vecs * per * 4 * s.team + (s.team > 32 ? s.teams * 64 * kMaxWarps : 0);
     s.stages = 1;

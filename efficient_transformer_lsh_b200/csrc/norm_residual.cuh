@@ -519,7 +519,7 @@ __device__ __forceinline__ float inv_std(float sum_sq, float inv_d, float eps) {
 // one stage has to fit, and a token's vectors have to lie within 2^31 elements
 // of its first.
 struct SubShape {
-  int team, teams, threads, tok, groups, tokens, parts, stages, vecs, smem;
+  int per, team, teams, threads, tok, groups, tokens, parts, stages, vecs, smem;
   bool wide;
 };
 struct SubSize {
@@ -562,18 +562,22 @@ struct BwdSize {
   static constexpr int kCtas = SIG ? 3 : 2;
 };
 
-// Largest CTA and residency that a backward kernel is compiled for: a team of
-// up to a warp in CTAs of BwdSize; several warps with one token as many as 512
-// threads; with two tokens 256, 255 registers a thread.
-constexpr int kBwdMultiRoom = 256;
-template <class T, int V, int TEAM, int TOK, bool SIG>
+// Rows wider than 512 features take several warps in the backward, except a
+// norm's own (two sums a feature, not four), whose threads then hold 32.
+// Largest CTA that a backward kernel is compiled for, and the threads of an SM
+// at 255 registers.
+constexpr int kBwdWidePer = 32;
+constexpr int kBwdRoom = 256;
+template <class T, int V, int PER, int TEAM, int TOK, bool SIG>
 constexpr int bwd_threads() {
-  return TEAM != 0 ? (V == 1 ? kNarrowThreads : BwdSize<T, SIG>::kThreads)
-                   : TOK == 1 ? 32 * kMaxWarps : 256;
+  if (V == 1) return TEAM != 0 ? kNarrowThreads : 32 * kMaxWarps;
+  if (PER == kBwdWidePer) return kBwdRoom;
+  return TEAM != 0 ? BwdSize<T, SIG>::kThreads : TOK == 1 ? 32 * kMaxWarps : kBwdRoom;
 }
-template <class T, int V, int TEAM, int TOK, bool SIG>
+template <class T, int V, int PER, int TEAM, int TOK, bool SIG>
 constexpr int bwd_ctas() {
-  return TEAM != 0 ? (V == 1 ? 2 : BwdSize<T, SIG>::kCtas) : 1;
+  if (V == 1) return TEAM != 0 ? 2 : 1;
+  return TEAM != 0 && PER != kBwdWidePer ? BwdSize<T, SIG>::kCtas : 1;
 }
 
 template <class T>
