@@ -32,6 +32,8 @@ _KINDS = {None: _lib.LSH_NORM_NONE, "layer": _lib.LSH_NORM_LAYER, "rms": _lib.LS
 _GATES = {None: _lib.LSH_GATE_NONE, "vector": _lib.LSH_GATE_VECTOR,
           "sigmoid": _lib.LSH_GATE_SIGMOID}
 Layout = Union[str, Sequence[int]]
+_current_device = getattr(torch._C, "_cuda_getDevice", lambda: -1)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0)
 
 
 def _refuse(where: str, what: str):
@@ -54,6 +56,7 @@ class _Driver:
         if dev.type == "cuda" and dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
         self.device = dev
+        self._index = dev.index if dev.type == "cuda" else -1
         self._lib = _lib.lib()
         self._empty = self.B * self.H * self.L == 0
 
@@ -85,9 +88,10 @@ class _Driver:
         and the given strides. Decoding calls this for every token, so the
         usual case is one expression."""
         if t.dtype is self.tdtype and t.shape == self.shape and t.stride() == strides and \
-                t.device == self.device:
+                t.get_device() == self._index:
             return t.data_ptr()
-        if t.dtype is not self.tdtype or t.shape != self.shape or t.device != self.device:
+        if t.dtype is not self.tdtype or t.shape != self.shape or \
+                t.get_device() != self._index:
             _refuse(type(self).__name__, f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, "
                                          f"expected {self.tdtype} {self.shape} on {self.device}")
         if not self._empty:
@@ -102,27 +106,29 @@ class _Driver:
         """Address of a contiguous parameter (None: none)."""
         if t is None:
             return None
-        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == self.device:
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and \
+                t.get_device() == self._index:
             return t.data_ptr()
         _refuse(type(self).__name__, f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, "
                                      f"expected contiguous {dtype} {shape} on {self.device}")
 
-    def _call(self, fn, *args):
-        """fn(*args, stream) with the driver's device current; a stream of None
-        is that device's current stream."""
-        here = torch._C._cuda_getDevice()
-        if here == self.device.index:
-            stream = args[-1]
-            if stream is None:
-                stream = torch._C._cuda_getCurrentRawStream(here)
-            elif not isinstance(stream, int):
-                stream = stream.cuda_stream
-            code = fn(*args[:-1], stream)
-            if code != 0:
-                raise _lib.LshError(code, type(self).__name__)
-        else:
-            with torch.cuda.device(self.device):
-                self._call(fn, *args)
+    def _away(self):
+        """Whether another device than the driver's is the current one."""
+        return self._index >= 0 and _current_device() != self._index
+
+    def _there(self, method, *args, **kw):
+        with torch.cuda.device(self.device):
+            return method(*args, **kw)
+
+    def _stream(self, stream):
+        """Handle of a stream; None is the device's current one."""
+        if stream is None:
+            return _current_stream(self._index)
+        return stream if isinstance(stream, int) else stream.cuda_stream
+
+    def _ok(self, code):
+        if code != 0:
+            raise _lib.LshError(code, type(self).__name__)
 
     def _sized(self, n):
         if n == 0 and not self._empty:
@@ -155,34 +161,42 @@ class Norm(_Driver):
         self.p = _lib.make_norm_problem(B, H, L, d, dtype, _KINDS[kind], eps, self.sx[:3],
                                         self.sh[:3])
         self.ws_bytes = self._sized(_lib.lsh_norm_bwd_workspace_size(self.p))
-        self._p = ctypes.byref(self.p)
+        self._p, self._norm_fwd = ctypes.byref(self.p), self._lib.lsh_norm_fwd
         self._D = (self.H * self.d,)
         self.h = self._buffer(self.sh)
+        self._h = self.h.data_ptr()   # of the driver's own buffer
         self.dx = self._buffer(self.sx)
         self.dw = torch.empty(self._D, dtype=torch.float32, device=self.device)
         self.db = torch.empty_like(self.dw)
         self.ws = self._workspace(self.ws_bytes)
 
     def forward(self, x, w=None, b=None, out=None, stream=None):
-        h = self.h if out is None else out
+        if self._away():
+            return self._there(self.forward, x, w, b, out, stream)
         D = self._D
-        self._call(self._lib.lsh_norm_fwd, self._p, self._act(x, self.sx, "x"),
-                   self._vec(w, D, "w"), self._vec(b, D, "b"), self._act(h, self.sh, "out"), stream)
+        h = self.h if out is None else out
+        self._ok(self._norm_fwd(
+            self._p, self._act(x, self.sx, "x"), None if w is None else self._vec(w, D, "w"),
+            None if b is None else self._vec(b, D, "b"),
+            self._h if out is None else self._act(out, self.sh, "out"), self._stream(stream)))
         return h
 
     def backward(self, x, dh, w=None, b=None, dres=None, out=None, stream=None):
         """(dx, dw, db): gradients of sum(h * dh), with ``dres`` (the gradient
         that reaches x past the norm) added to dx. dw and db are formed where w
         and b are given, else None."""
+        if self._away():
+            return self._there(self.backward, x, dh, w, b, dres, out, stream)
         dx = self.dx if out is None else out
         D = self._D
         self._vec(b, D, "b")
         dw, db = None if w is None else self.dw, None if b is None else self.db
-        self._call(self._lib.lsh_norm_bwd, self._p, self._act(x, self.sx, "x"),
-                   self._vec(w, D, "w"), self._act(dh, self.sh, "dh"),
-                   None if dres is None else self._act(dres, self.sx, "dres"),
-                   self._act(dx, self.sx, "out"), _lib._ptr(dw), _lib._ptr(db),
-                   self.ws.data_ptr(), self.ws_bytes, stream)
+        self._ok(self._lib.lsh_norm_bwd(
+            self._p, self._act(x, self.sx, "x"), self._vec(w, D, "w"),
+            self._act(dh, self.sh, "dh"),
+            None if dres is None else self._act(dres, self.sx, "dres"),
+            self._act(dx, self.sx, "out"), _lib._ptr(dw), _lib._ptr(db), self.ws.data_ptr(),
+            self.ws_bytes, self._stream(stream)))
         return dx, dw, db
 
 
@@ -207,10 +221,12 @@ class Dropout(_Driver):
         self.dx = self._buffer(self.sx)
 
     def _run(self, q, src, sx, dst, sy, seed, offset, counter, stream):
-        self._call(self._lib.lsh_dropout_fwd, ctypes.byref(q), self._act(src, sx, "input"),
-                   _seed(seed, "Dropout"), _seed(offset, "Dropout"),
-                   self._vec(counter, (1,), "counter", torch.int64), self._act(dst, sy, "out"),
-                   stream)
+        if self._away():
+            return self._there(self._run, q, src, sx, dst, sy, seed, offset, counter, stream)
+        self._ok(self._lib.lsh_dropout_fwd(
+            ctypes.byref(q), self._act(src, sx, "input"), _seed(seed, "Dropout"),
+            _seed(offset, "Dropout"), self._vec(counter, (1,), "counter", torch.int64),
+            self._act(dst, sy, "out"), self._stream(stream)))
         return dst
 
     def forward(self, x, seed, offset=0, counter=None, out=None, stream=None):
@@ -249,12 +265,14 @@ class Residual(_Driver):
         # x from y: the same branch taken off, and the scale undone
         self.p_restore = problem(None, -alpha / beta, 1.0 / beta) if beta != 0 else None
         self.ws_bytes = self._sized(_lib.lsh_residual_bwd_workspace_size(self.p))
-        self._p = ctypes.byref(self.p)
+        self._p, self._residual_fwd = ctypes.byref(self.p), self._lib.lsh_residual_fwd
         self._D = (self.H * self.d,)
         self.gate_shape = (self.B, self._D[0]) if gate_batch else self._D
         f32 = dict(dtype=torch.float32, device=self.device)
         self.y = self._buffer(self.sx)
         self.h = self._buffer(self.sx) if norm else None
+        # of the driver's own buffers
+        self._y, self._h = self.y.data_ptr(), None if self.h is None else self.h.data_ptr()
         self.x = self._buffer(self.sx)
         self.dx = self._buffer(self.sx)
         self.df = self._buffer(self.sf)
@@ -282,19 +300,23 @@ class Residual(_Driver):
         if not self.norm and (w is not None or b is not None):
             _refuse("Residual", "w, b without a norm of y")
         D, vec = self._D, self._vec
-        return (gate, vec(w_post, D, "w_post"), vec(b_post, D, "b_post"), vec(w, D, "w"),
-                vec(b, D, "b"))
+        return (gate, None if w_post is None else vec(w_post, D, "w_post"),
+                None if b_post is None else vec(b_post, D, "b_post"),
+                None if w is None else vec(w, D, "w"), None if b is None else vec(b, D, "b"))
 
     def forward(self, x, f, gate=None, w_post=None, b_post=None, w=None, b=None, seed=0, offset=0,
                 counter=None, stream=None):
         """(y, h); h is None without a norm."""
-        y, h = self.y, self.h
-        self._call(self._lib.lsh_residual_fwd, self._p, self._act(x, self.sx, "x"),
-                   self._act(f, self.sf, "f"), *self._params(gate, w_post, b_post, w, b),
-                   _seed(seed, "Residual"), _seed(offset, "Residual"),
-                   self._vec(counter, (1,), "counter", torch.int64), y.data_ptr(),
-                   None if h is None else h.data_ptr(), stream)
-        return y, h
+        if self._away():
+            return self._there(self.forward, x, f, gate, w_post, b_post, w, b, seed, offset,
+                               counter, stream)
+        self._ok(self._residual_fwd(
+            self._p, self._act(x, self.sx, "x"), self._act(f, self.sf, "f"),
+            *self._params(gate, w_post, b_post, w, b), _seed(seed, "Residual"),
+            _seed(offset, "Residual"),
+            None if counter is None else self._vec(counter, (1,), "counter", torch.int64),
+            self._y, self._h, self._stream(stream)))
+        return self.y, self.h
 
     def restore(self, y, f, gate=None, w_post=None, b_post=None, seed=0, offset=0, counter=None,
                 stream=None):
@@ -302,11 +324,14 @@ class Residual(_Driver):
         from its output, with the same branch, seed and offset."""
         if self.p_restore is None:
             _refuse("Residual", "beta = 0 cannot be undone")
-        self._call(self._lib.lsh_residual_fwd, ctypes.byref(self.p_restore),
-                   self._act(y, self.sx, "y"), self._act(f, self.sf, "f"),
-                   *self._params(gate, w_post, b_post, None, None), _seed(seed, "Residual"),
-                   _seed(offset, "Residual"), self._vec(counter, (1,), "counter", torch.int64),
-                   self.x.data_ptr(), None, stream)
+        if self._away():
+            return self._there(self.restore, y, f, gate, w_post, b_post, seed, offset, counter,
+                               stream)
+        self._ok(self._residual_fwd(
+            ctypes.byref(self.p_restore), self._act(y, self.sx, "y"), self._act(f, self.sf, "f"),
+            *self._params(gate, w_post, b_post, None, None), _seed(seed, "Residual"),
+            _seed(offset, "Residual"), self._vec(counter, (1,), "counter", torch.int64),
+            self.x.data_ptr(), None, self._stream(stream)))
         return self.x
 
     def backward(self, dy, f, y=None, dh=None, gate=None, w_post=None, b_post=None, w=None, b=None,
@@ -315,6 +340,9 @@ class Residual(_Driver):
         sum(h * dh). y (forward's) and dh are needed with a norm, where dy may
         be None (zeros). Parameter gradients are formed for the parameters
         given, else None."""
+        if self._away():
+            return self._there(self.backward, dy, f, y, dh, gate, w_post, b_post, w, b, seed,
+                               offset, counter, stream)
         p_gate, p_wp, p_bp, p_w, _ = self._params(gate, w_post, b_post, w, b)
         p_y = p_dh = None
         if self.norm:
@@ -327,12 +355,12 @@ class Residual(_Driver):
         db_post = None if b_post is None else self.db_post
         dw, db = None if w is None else self.dw, None if b is None else self.db
         ptr = _lib._ptr
-        self._call(self._lib.lsh_residual_bwd, self._p,
-                   None if dy is None else self._act(dy, self.sx, "dy"), p_dh, p_y,
-                   self._act(f, self.sf, "f"), p_gate, p_wp, p_bp, p_w, _seed(seed, "Residual"),
-                   _seed(offset, "Residual"), self._vec(counter, (1,), "counter", torch.int64),
-                   self.dx.data_ptr(), self.df.data_ptr(), ptr(self.dgate), ptr(dw_post),
-                   ptr(db_post), ptr(dw), ptr(db), self.ws.data_ptr(), self.ws_bytes, stream)
+        self._ok(self._lib.lsh_residual_bwd(
+            self._p, None if dy is None else self._act(dy, self.sx, "dy"), p_dh, p_y,
+            self._act(f, self.sf, "f"), p_gate, p_wp, p_bp, p_w, _seed(seed, "Residual"),
+            _seed(offset, "Residual"), self._vec(counter, (1,), "counter", torch.int64),
+            self.dx.data_ptr(), self.df.data_ptr(), ptr(self.dgate), ptr(dw_post), ptr(db_post),
+            ptr(dw), ptr(db), self.ws.data_ptr(), self.ws_bytes, self._stream(stream)))
         return self.dx, self.df, self.dgate, dw_post, db_post, dw, db
 
 
@@ -413,6 +441,8 @@ class Rotary(_Driver):
         self.dx = self._buffer(self.sx)
 
     def _run(self, fn, src, ss, dst, sd, pos, pos0, stream):
+        if self._away():
+            return self._there(self._run, fn, src, ss, dst, sd, pos, pos0, stream)
         q = self._p[0]
         if pos is not None:
             if pos.dim() == 2:
@@ -420,8 +450,8 @@ class Rotary(_Driver):
                 pos = self._vec(pos, (self.B, self.L), "pos", torch.int32)
             else:
                 pos = self._vec(pos, (self.L,), "pos", torch.int32)
-        self._call(fn, q, self._act(src, ss, "input"), self._turns, pos, int(pos0),
-                   self._act(dst, sd, "out"), stream)
+        self._ok(fn(q, self._act(src, ss, "input"), self._turns, pos, int(pos0),
+                    self._act(dst, sd, "out"), self._stream(stream)))
         return dst
 
     def forward(self, x, pos=None, pos0=0, out=None, stream=None):
@@ -437,6 +467,8 @@ class Rotary(_Driver):
         """dx = (backward of dqk) + dv for an activation that fed the attention
         both turned and as it is; dqk, dv: the attention's float32 gradients,
         contiguous."""
+        if self._away():
+            return self._there(self.backward_sum, dqk, dv, pos, pos0, out, stream)
         dx = self.dx if out is None else out
         f32 = torch.float32
         q, addr = self._p[0], None
@@ -444,9 +476,9 @@ class Rotary(_Driver):
             two = pos.dim() == 2
             q = self._p[1] if two else q
             addr = self._vec(pos, (self.B, self.L) if two else (self.L,), "pos", torch.int32)
-        self._call(self._lib.lsh_rope_bwd_sum, q, self._vec(dqk, self.shape, "dqk", f32),
-                   self._vec(dv, self.shape, "dv", f32), self._turns, addr, int(pos0),
-                   self._act(dx, self.sx, "out"), stream)
+        self._ok(self._lib.lsh_rope_bwd_sum(
+            q, self._vec(dqk, self.shape, "dqk", f32), self._vec(dv, self.shape, "dv", f32),
+            self._turns, addr, int(pos0), self._act(dx, self.sx, "out"), self._stream(stream)))
         return dx
 
 
@@ -541,14 +573,15 @@ class ReversibleLayer(_Driver):
         return n, q, self.attn.attend(q, n, None, stream)[0]
 
     def _feed(self, m, w, stream):
-        self._call(self._lib.lsh_ff_fwd, ctypes.byref(self.f), m.data_ptr(), w["W1"].data_ptr(),
-                   w["b1"].data_ptr(), w["W2"].data_ptr(), w["b2"].data_ptr(), None,
-                   self.g.data_ptr(), self.ff_ws.data_ptr(), self.ff_ws_bytes, stream)
+        _lib.lsh_ff_fwd(self.f, m, w["W1"], w["b1"], w["W2"], w["b2"], None, self.g, self.ff_ws,
+                        self.ff_ws_bytes, stream)
         return self.g
 
     def forward(self, x1, x2, R, w, seed=0, offset=0, counter=None, pos0=0, stream=None):
         """(y1, y2); R [n_rounds, 64, n_buckets / 2] bf16. Token l of every
         sequence has position pos0 + l."""
+        if self._away():
+            return self._there(self.forward, x1, x2, R, w, seed, offset, counter, pos0, stream)
         self._check(w)
         o1, o2 = self._offsets(offset)
         head = self._strides("head")
@@ -567,6 +600,9 @@ class ReversibleLayer(_Driver):
         """(x1, x2, dx1, dx2, grads): the inputs rebuilt from the outputs and
         the gradients of sum(y1 dy1) + sum(y2 dy2); grads is a dict like w, all
         float32. Uses the permutation of the last forward of this driver."""
+        if self._away():
+            return self._there(self.backward, y1, y2, dy1, dy2, w, seed, offset, counter, pos0,
+                               stream)
         self._check(w)
         o1, o2 = self._offsets(offset)
         rng = dict(seed=seed, counter=counter, stream=stream)
@@ -576,11 +612,9 @@ class ReversibleLayer(_Driver):
         g = self._feed(m, w, stream)
         x2 = self.join2.restore(y2, g, **b2, offset=o2, **rng)
         dx2, dg, *d2 = self.join2.backward(dy2, g, **b2, offset=o2, **rng)
-        self._call(self._lib.lsh_ff_bwd, ctypes.byref(self.f), m.data_ptr(), w["W1"].data_ptr(),
-                   w["b1"].data_ptr(), w["W2"].data_ptr(), w["b2"].data_ptr(), dg.data_ptr(), None,
-                   None, None, self.dm.data_ptr(), self.dW1.data_ptr(), self.db1.data_ptr(),
-                   self.dW2.data_ptr(), self.db2.data_ptr(), self.ff_ws.data_ptr(),
-                   self.ff_ws_bytes, stream)
+        _lib.lsh_ff_bwd(self.f, m, w["W1"], w["b1"], w["W2"], w["b2"], dg, None, None, None,
+                        self.dm, self.dW1, self.db1, self.dW2, self.db2, self.ff_ws,
+                        self.ff_ws_bytes, stream)
         # attention half: F(norm1(x2)) again, x1 = y1 - branch(F), F's gradients
         n, q, f = self._attend(x2, w, pos0, stream)
         x1 = self.join1.restore(y1, f, **b1, offset=o1, **rng)
@@ -591,8 +625,7 @@ class ReversibleLayer(_Driver):
             dn = self.rope.backward_sum(dqk, dv, pos0=pos0, out=self.dn, stream=stream)
         else:
             dn = self.dn
-            self._call(self._lib.lsh_rope_bwd_sum, ctypes.byref(self._sum), dqk.data_ptr(),
-                       dv.data_ptr(), None, None, 0, dn.data_ptr(), stream)
+            _lib.lsh_rope_bwd_sum(self._sum, dqk, dv, None, None, 0, dn, stream)
         _, dw, db = self.norm1.backward(x2, dn, w["norm1_w"], w.get("norm1_b"), dres=dx2,
                                         out=self.dx2, stream=stream)
         grads = dict(W1=self.dW1, b1=self.db1, W2=self.dW2, b2=self.db2, norm1_w=dw, norm1_b=db,
