@@ -36,7 +36,9 @@ struct DropArgs {
   const uint64_t* counter;
 };
 
-template <class T, int V, bool FLAT>
+// DIMS: 3, or 1 where all dimensions merge, or 0 where the rows also follow on
+// in x, y and the counters without a gap.
+template <class T, int V, int DIMS>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant__ DropArgs a) {
   stream_wait();
   let_next_start();
@@ -51,14 +53,20 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) {
       const int j = j0 + k * kThreads;
-      if (j < n) {
+      if (DIMS == 0 && j < n) {
+        c[k] = 0;
+        const int64_t u = (int64_t)row0 * a.upr.d + j;
+        out[k] = u * V;
+        ctr[k] = a.ctr0 + u;
+        r[k].load((const T*)a.x + out[k]);
+      } else if (j < n) {
         const int rr = (int)a.upr.div((uint32_t)j);
         c[k] = (j - rr * (int)a.upr.d) * V;
         const int row = row0 + rr;
         int64_t in = c[k];
         out[k] = c[k];
         ctr[k] = a.ctr0 + (uint32_t)c[k] / 8;
-        if constexpr (FLAT) {
+        if constexpr (DIMS == 1) {
           in += row * a.sx[0];
           out[k] += row * a.sy[0];
           ctr[k] += (uint32_t)row * a.sc[0];
@@ -90,9 +98,11 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant
 }
 
 template <class T, int V>
-cudaError_t run(const DropArgs& a, bool flat, cudaStream_t s) {
+cudaError_t run(const DropArgs& a, int dims, cudaStream_t s) {
   note_launch();
-  return launch_overlapped(flat ? dropout_kernel<T, V, true> : dropout_kernel<T, V, false>,
+  return launch_overlapped(dims == 0   ? dropout_kernel<T, V, V == 8 ? 0 : 1>
+                           : dims == 1 ? dropout_kernel<T, V, 1>
+                                       : dropout_kernel<T, V, 3>,
                            dim3((unsigned)((a.rows + a.tile - 1) / a.tile)), kThreads, 0, s, a);
 }
 
@@ -130,9 +140,11 @@ cudaError_t launch_dropout(const lsh_dropout_problem& q, uint32_t t, float scale
   a.tile = std::max(1, kThreads * kUnits / (int)a.upr.d);
   a.t = t, a.scale = scale, a.key = PhiloxKeys(seed), a.offset = offset, a.counter = counter;
   a.ctr0 = q.slice0 * head;
+  const bool dense = wide && m == 0 && d[0].x == q.d && d[0].y == q.d && d[0].c == gpr;
+  const int dims = dense ? 0 : m == 0 ? 1 : 3;
   if (q.dtype == LSH_BF16)
-    return wide ? run<__nv_bfloat16, 8>(a, m == 0, s) : run<__nv_bfloat16, 1>(a, m == 0, s);
-  return wide ? run<float, 8>(a, m == 0, s) : run<float, 1>(a, m == 0, s);
+    return wide ? run<__nv_bfloat16, 8>(a, dims, s) : run<__nv_bfloat16, 1>(a, dims, s);
+  return wide ? run<float, 8>(a, dims, s) : run<float, 1>(a, dims, s);
 }
 
 }  // namespace lsh
