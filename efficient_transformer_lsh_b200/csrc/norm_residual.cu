@@ -125,25 +125,31 @@ struct FinalArgs {
 // i + 64, ... of a group, all loads in flight, then a warp's four, then the
 // warps in order. (32 features and 32 threads each: 9.2 us for 444 rows of 512
 // features, the latency of two rounds of loads on 16 SMs.)
-constexpr int kFinalCols = 8, kFinalRows = 64;
+constexpr int kFinalCols = 8, kFinalRows = 64, kFinalWarps = kFinalCols * kFinalRows / 32;
 __global__ void __launch_bounds__(kFinalCols* kFinalRows)
 sub_final_kernel(const __grid_constant__ FinalArgs a) {
-  __shared__ float buf[2][kFinalCols * kFinalRows / 32][kFinalCols];
+  __shared__ float buf[2][kFinalWarps][kFinalCols];
   stream_wait();
   let_next_start();
-  const int col = threadIdx.x % kFinalCols, i = threadIdx.x / kFinalCols, w = threadIdx.x >> 5;
+  const int col = threadIdx.x % kFinalCols, i = threadIdx.x / kFinalCols;
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = blockIdx.x * kFinalCols + col;
   const bool on = c < a.D;
   const bool branch = a.norm ? blockIdx.y == 1 : true;
   const int v0 = branch && a.norm ? 2 : 0;
   const int64_t row = (int64_t)a.vecs * a.D;
-  float t1 = 0.f, t0 = 0.f;   // the first threads: totals over the groups
-  for (int g = 0; g < a.groups; ++g) {
+  // Few groups: one after the other, 64 threads a feature each. Many (a gate
+  // for each of 16 sequences or more): a warp takes every 16th group, which
+  // has few rows then, with four threads a feature.
+  const bool many = a.groups >= kFinalWarps;
+  const int lanes = many ? kFinalRows / kFinalWarps : kFinalRows;
+  float t1 = 0.f, t0 = 0.f;   // totals over the groups
+  for (int g = many ? w : 0; g < a.groups; g += many ? kFinalWarps : 1) {
     float s1 = 0.f, s0 = 0.f;
     if (on) {
       const float* r = a.part + (int64_t)g * a.parts * row + v0 * a.D + c;
 #pragma unroll 8
-      for (int p = i; p < a.parts; p += kFinalRows) {
+      for (int p = i % lanes; p < a.parts; p += lanes) {
         s1 += __ldcg(r + p * row);
         s0 += __ldcg(r + p * row + a.D);
       }
@@ -153,31 +159,45 @@ sub_final_kernel(const __grid_constant__ FinalArgs a) {
       s1 += __shfl_xor_sync(0xffffffffu, s1, o);
       s0 += __shfl_xor_sync(0xffffffffu, s0, o);
     }
-    if ((threadIdx.x & 31) < kFinalCols) {
-      buf[0][w][col] = s1;
-      buf[1][w][col] = s0;
-    }
-    __syncthreads();
-    if (i == 0 && on) {
+    if (!many) {
+      __syncthreads();
+      if (lane < kFinalCols) {
+        buf[0][w][col] = s1;
+        buf[1][w][col] = s0;
+      }
+      __syncthreads();
       s1 = s0 = 0.f;
 #pragma unroll
-      for (int k = 0; k < kFinalCols * kFinalRows / 32; ++k) {
+      for (int k = 0; k < kFinalWarps; ++k) {
         s1 += buf[0][k][col];
         s0 += buf[1][k][col];
       }
-      if (branch) {
-        const float gate = a.gv ? a.gv[(a.gate_batch ? (int64_t)g * a.D : 0) + c] : 1.f;
-        if (a.dgate && (a.gate_batch || a.groups == 1))
-          a.dgate[(int64_t)g * a.D + c] =
-              (a.wp ? a.wp[c] : 1.f) * s1 + (a.bp ? a.bp[c] * s0 : 0.f);
-        t1 = fmaf(gate, s1, t1);
-        t0 = fmaf(gate, s0, t0);
-      } else {
-        t1 += s1;
-        t0 += s0;
-      }
+    }
+    if (branch && on) {
+      const float gate = a.gv ? a.gv[(a.gate_batch ? (int64_t)g * a.D : 0) + c] : 1.f;
+      if (a.dgate && lane < kFinalCols && (many || w == 0))
+        a.dgate[(int64_t)g * a.D + c] =
+            (a.wp ? a.wp[c] : 1.f) * s1 + (a.bp ? a.bp[c] * s0 : 0.f);
+      t1 = fmaf(gate, s1, t1);
+      t0 = fmaf(gate, s0, t0);
+    } else {
+      t1 += s1;
+      t0 += s0;
+    }
+  }
+  if (many) {
+    __syncthreads();
+    if (lane < kFinalCols) {
+      buf[0][w][col] = t1;
+      buf[1][w][col] = t0;
     }
     __syncthreads();
+    t1 = t0 = 0.f;
+#pragma unroll
+    for (int k = 0; k < kFinalWarps; ++k) {
+      t1 += buf[0][k][col];
+      t0 += buf[1][k][col];
+    }
   }
   if (i == 0 && on) {
     float* o1 = branch ? a.dwp : a.dw;

@@ -256,9 +256,17 @@ lsh_status lsh_rev_bwd(const lsh_problem* p, const lsh_ff_problem* f, const void
  * strides are multiples of 16 bytes and d of 8, the wide-access kernels run.
  *
  * An output activation may be the same array (pointer and strides) as an
- * activation input of the same call; any other overlap, and two outputs that
- * overlap, give undefined values. At most 2^30 rows (B H L). B*L == 0 launches no activation kernel; parameter gradients are
- * then written as zeros. Nothing here uses the device status word.
+ * activation input of the same call, except that lsh_residual_bwd's dx may
+ * not be f or z; any other overlap, and two outputs that overlap, give
+ * undefined values. At most 2^30 rows (B H L). B*L == 0 launches no activation
+ * kernel; parameter gradients are then written as zeros. Nothing here uses the
+ * device status word. NaN and infinities stay within their token (norms) or
+ * element (the rest). A norm's sums of squares are float32: |x| sqrt(D) stays
+ * below about 1e19. A norm needs a token's H heads in one call: ranks that
+ * share a problem split it by batch.
+ *
+ * Launches are programmatic-dependent: a kernel may be set up while earlier
+ * work of its stream runs, and waits for all of it before it touches memory.
  */
 typedef struct {
   int64_t b, h, l;
@@ -332,7 +340,8 @@ lsh_status lsh_dropout_fwd(const lsh_dropout_problem* q, const void* x, uint64_t
  *   written). gate: none; LSH_GATE_VECTOR, a float32 vector [D], or [B, D]
  *   with gate_batch; LSH_GATE_SIGMOID, gate = 1 / (1 + exp(-z)) of an
  *   activation z like f. drop as in lsh_dropout_fwd (p = 0: none; element
- *   indices of [B, H, L, d]). h is the norm of y as stored, bit for bit what
+ *   indices of [B, H, L, d]). h is the norm of y as stored, and where both
+ *   calls run the wide-access kernels (or both the others) bit for bit what
  *   lsh_norm_fwd(y) gives: a reversible layer recomputes h from the stored y.
  *   w, b, w_post, b_post may be NULL (ones, zeros).
  *   With (alpha, beta) replaced by (-alpha/beta, 1/beta), x := y and no norm

@@ -173,6 +173,9 @@ RES_CASES = [
     (1, 100, 3, 33, "f32", "rms", "layer", "sigmoid", False, 0.2, 1.0, 1.0, "odd", "head", 0),
     (1, 8, 21, 64, "bf16", "rms", "layer", "sigmoid", False, 0.2, 1.0, 1.0, "head", "head", 1),
     (1, 8, 9001, 64, "bf16", "layer", "layer", "vector", False, 0.1, 0.5, 1.0, "head", "head", 0),
+    (100, 2, 3, 64, "bf16", "layer", "rms", "vector", True, 0.1, 1.0, 1.0, "head", "head", 0),
+    (17, 1, 40, 64, "f32", None, "layer", "vector", True, 0.0, 1.0, 1.0, "head", "head", 0),
+    (16, 9, 1, 64, "bf16", "rms", None, "vector", True, 0.0, 1.0, 1.0, "token", "token", 0),
 ]
 
 
