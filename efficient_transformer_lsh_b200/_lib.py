@@ -320,9 +320,7 @@ def lsh_rev_bwd(p: lsh_problem, f: lsh_ff_problem, y1, y2, dy1, dy2, perm, W1, b
                              _ptr(dy2), _ptr(perm), _ptr(W1), _ptr(b1), _ptr(W2), _ptr(b2),
                              _ptr(x1), _ptr(x2), _ptr(dx1), _ptr(dx2), _ptr(dW1), _ptr(db1),
                              _ptr(dW2), _ptr(db2), _ptr(ws), int(ws_bytes), _stream(stream)),
-           "lsh_rev_bwd", "lsh_norm_fwd", "lsh_norm_bwd_workspace_size", "lsh_norm_bwd",
-           "lsh_dropout_fwd", "lsh_residual_fwd", "lsh_residual_bwd_workspace_size",
-           "lsh_residual_bwd", "lsh_rope_fwd", "lsh_rope_bwd", "lsh_rope_bwd_sum")
+           "lsh_rev_bwd")
 
 
 def lsh_device_status(stream=None) -> int:
