@@ -60,7 +60,8 @@ sub_bwd_kernel(const __grid_constant__ SubArgs a) {
   let_next_start();
   constexpr bool post = BRANCH && POST, sig = BRANCH && SIG;
   const float* gv = a.gv ? a.gv + (int64_t)at.group * (a.gate_batch ? a.D : 0) : nullptr;
-  const bool has1 = BRANCH && (a.wp || gv), has0 = sig && a.bp;
+  // with a norm of f always there: it also keeps features past D out of the sums
+  const bool has1 = post || (BRANCH && gv), has0 = sig && a.bp;
   // the ring's tensors: y dh, dy, f, z
   const int i_dy = NORM ? 2 : 0, i_f = i_dy + (a.dy ? 1 : 0), i_z = i_f + 1;
   const int tensors = i_f + BRANCH + sig;
@@ -222,9 +223,13 @@ sub_bwd_kernel(const __grid_constant__ SubArgs a) {
     if (a.dx) {
 #pragma unroll
       for (int j = 0; j < TOK; ++j) {
+        if (BRANCH && a.beta != 1.f) {
 #pragma unroll
-        for (int i = 0; i < P; ++i) hat[j][i] = BRANCH ? mul2(q[j][i], pk(a.beta, a.beta)) : q[j][i];
-        at.template put<false>(a.dx, a.sx, at.ox, b[j], l[j], live[j], hat[j]);
+          for (int i = 0; i < P; ++i) hat[j][i] = mul2(q[j][i], pk(a.beta, a.beta));
+          at.template put<false>(a.dx, a.sx, at.ox, b[j], l[j], live[j], hat[j]);
+        } else {
+          at.template put<false>(a.dx, a.sx, at.ox, b[j], l[j], live[j], q[j]);
+        }
       }
     }
     if constexpr (BRANCH) {
@@ -245,12 +250,15 @@ sub_bwd_kernel(const __grid_constant__ SubArgs a) {
           at.team_sum(s);
 #pragma unroll
           for (int j = 0; j < TOK; ++j) r_f[j] = inv_std(s[j], a.inv_d, a.eps_post);
-        } else if (lf) {
-#pragma unroll
-          for (int j = 0; j < TOK; ++j) at.center(hat[j], mean_f[j]);
         }
+        // fhat = f r - mean r in one step (past D it is not 0, but q is there)
 #pragma unroll
-        for (int j = 0; j < TOK; ++j) scale_all(hat[j], r_f[j]);
+        for (int j = 0; j < TOK; ++j) {
+          const float m = NORM && lf ? -mean_f[j] * r_f[j] : 0.f;
+          const f2 r2 = pk(r_f[j], r_f[j]), m2 = pk(m, m);
+#pragma unroll
+          for (int i = 0; i < P; ++i) hat[j][i] = fma2(hat[j][i], r2, m2);
+        }
       }
 #pragma unroll
       for (int j = 0; j < TOK; ++j) {

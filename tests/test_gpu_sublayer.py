@@ -259,6 +259,33 @@ def test_residual(case):
         _close(dx, ref["dx"], dtype, abs(beta) * tm)
 
 
+@pytest.mark.parametrize("H,d,dtype,post,norm", [
+    (5, 64, "bf16", "layer", "layer"), (3, 64, "f32", "rms", "layer"), (9, 64, "bf16", "rms", "layer"),
+    (5, 7, "bf16", "layer", "layer"), (11, 64, "f32", "layer", "rms")])
+def test_residual_without_parameters(H, d, dtype, post, norm):
+    """Norms with no weights on rows that do not fill their threads: the
+    features past the row's end stay out of its sums."""
+    from efficient_transformer_lsh_b200 import sublayer as sl
+    g = np.random.default_rng(H)
+    B, L, eps = 2, 21, 1e-5
+    shape = (B, H, L, d)
+    (f, f_), (y, y_), (dy, dy_), (dh, dh_) = (_put(g.standard_normal(shape) + 0.4, dtype)
+                                              for _ in range(4))
+    r = sl.Residual(B, H, L, post, norm, None, dtype=dtype, d=d)
+    dx, df, *rest = r.backward(dy, f, y=y, dh=dh)
+    assert all(t is None for t in rest)
+    ref = orc.residual_backward(dy_, dh_, y_, f_, post, norm, eps=eps)
+    m, _ = _norm_back_mag(y_, norm, eps, None, dh_)
+    tm = np.abs(dy_) + m
+    _close(dx, ref["dx"], dtype, tm)
+    _close(df, ref["df"], dtype, _norm_back_mag(f_, post, eps, None, tm)[0], 2 * K)
+    out, h = r.forward(y, f)
+    want = orc.residual_forward(y_, f_, post, eps=eps)
+    _close(out, want, dtype, np.abs(y_) + _norm_mag(f_, post, eps, None, None))
+    o = out.double().cpu().numpy()
+    _close(h, orc.norm_forward(o, norm, eps), dtype, _norm_mag(o, norm, eps, None, None))
+
+
 DROP_CASES = [(1, 1, 1, 64, "bf16", 0.1, "head", "head"), (7, 3, 401, 64, "f32", 0.25, "head", "head"),
               (2, 5, 33, 64, "bf16", 0.5, "token", "head"), (2, 3, 11, 7, "bf16", 0.3, "head", "odd"),
               (1, 2, 5, 20, "f32", 0.3, "odd", "token"), (1, 8, 4099, 64, "bf16", 0.1, "head", "head"),
