@@ -18,11 +18,12 @@ SubShape sub_shape(const SubCall& c, const SubSize& z) {
     if ((c.H - 1) * t->h + c.d > (int64_t)INT32_MAX) s.wide = false;
   int ctas, fixed;
   for (;;) {
-    const bool wide_norm = s.wide && z.backward && !c.branch && D > 32 * kBwdPer;
-    const int per = !s.wide ? kNarrowPer : wide_norm ? kBwdWidePer : z.per;
+    const bool wide_rows = s.wide && z.backward && D > 32 * kBwdPer &&
+                           (!c.branch || (c.dtype == LSH_BF16 && D <= kBwdWarpMax));
+    const int per = !s.wide ? kNarrowPer : wide_rows ? kBwdWidePer : z.per;
     const int threads = s.wide ? z.threads : kNarrowThreads;
     s.per = per;
-    s.tok = s.wide && !wide_norm ? z.tok : 1;
+    s.tok = s.wide && !wide_rows ? z.tok : 1;
     // threads of a token: a power of two up to a warp, then whole warps
     s.team = (D + per - 1) / per;
     if (s.team > 32) {
@@ -34,13 +35,17 @@ SubShape sub_shape(const SubCall& c, const SubSize& z) {
     } else {
       s.team = 32;
     }
-    // 512 threads of two tokens each do not fit the register file
-    if (s.team > 256) s.tok = 1;
+    // Teams of several warps take one token at a time, with more of them
+    // resident to cover their barriers (backward of 4 x 4096 tokens of 4096
+    // features: 212 us against 245 with two)
+    if (s.team > 32) s.tok = 1;
     s.teams = std::max(1, threads / s.team);
     s.threads = s.teams * s.team;
     // threads resident on an SM, by the registers of each form
     int room = 512;
-    if (wide_norm || (z.backward && s.wide && s.team > 32 && s.tok > 1)) room = kBwdRoom;
+    if (wide_rows) room = kBwdRoom;
+    else if (s.wide && z.backward && s.team > 32)
+      room = s.team <= kBwdTeam ? kBwdTeamRoom : kBwdBigRoom;
     else if (s.wide && (!z.backward || s.team <= 32)) room = z.ctas * threads;
     ctas = std::max(1, room / s.threads);
     fixed = z.vecs * per * 4 * s.team + (s.team > 32 ? s.teams * 64 * kMaxWarps : 0);

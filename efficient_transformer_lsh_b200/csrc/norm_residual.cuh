@@ -167,10 +167,11 @@ __device__ __forceinline__ void cp_wait_for(int pending) {
 // parameters, flags and addresses are read once for them, and a warp's teams
 // neighbouring ones; `live` is false for a token past the last, which a team
 // only goes along with.
-// TEAM: threads of a token up to a warp, or 0: whole warps, a.team threads.
+// TEAM: threads of a token up to a warp, or 0 or less: whole warps, a.team of
+// them.
 template <class T, int V, int PER, int TEAM, int TOK, int THREADS>
 struct Place {
-  static constexpr bool kMulti = TEAM == 0;
+  static constexpr bool kMulti = TEAM <= 0;
   static constexpr int NV = PER / V;
   static constexpr int P = PER / 2;                          // pairs
   static constexpr bool kRing = V > 1;
@@ -562,22 +563,29 @@ struct BwdSize {
   static constexpr int kCtas = SIG ? 3 : 2;
 };
 
-// Rows wider than 512 features take several warps in the backward, except a
-// norm's own (two sums a feature, not four), whose threads then hold 32.
-// Largest CTA that a backward kernel is compiled for, and the threads of an SM
-// at 255 registers.
-constexpr int kBwdWidePer = 32;
-constexpr int kBwdRoom = 256;
-template <class T, int V, int PER, int TEAM, int TOK, bool SIG>
+// Rows wider than 512 features in the backward. A norm's own (two sums a
+// feature, not four) holds 32 features a thread at any width, and so does
+// bf16 with a branch up to 1024, where that makes a warp of a token (2 x 12288
+// tokens of 1024 features: 77 us; 98 with two warps of 16 features a thread).
+// Wider ones take several warps of 16: 168 registers up to 192 threads, else
+// 128 for two CTAs an SM (12288 tokens of 2048 features: 106 us at 168, 116 at
+// 128; 16384 of 4096: 264 and 212).
+constexpr int kBwdWidePer = 32, kBwdWarpMax = 1024;
+constexpr int kBwdRoom = 256;                           // threads an SM at 255 registers
+constexpr int kBwdTeam = 192, kBwdTeamRoom = 384;       // at 168
+constexpr int kBwdBigRoom = 512;                        // at 128
+constexpr int kBig = -1;                                // TEAM of the last
+template <class T, int V, int PER, int TEAM, bool SIG>
 constexpr int bwd_threads() {
   if (V == 1) return TEAM != 0 ? kNarrowThreads : 32 * kMaxWarps;
   if (PER == kBwdWidePer) return kBwdRoom;
-  return TEAM != 0 ? BwdSize<T, SIG>::kThreads : TOK == 1 ? 32 * kMaxWarps : kBwdRoom;
+  return TEAM == kBig ? kBwdBigRoom : TEAM == 0 ? kBwdTeam : BwdSize<T, SIG>::kThreads;
 }
-template <class T, int V, int PER, int TEAM, int TOK, bool SIG>
+template <class T, int V, int PER, int TEAM, bool SIG>
 constexpr int bwd_ctas() {
   if (V == 1) return TEAM != 0 ? 2 : 1;
-  return TEAM != 0 && PER != kBwdWidePer ? BwdSize<T, SIG>::kCtas : 1;
+  if (PER == kBwdWidePer || TEAM == kBig) return 1;
+  return TEAM == 0 ? kBwdTeamRoom / kBwdTeam : BwdSize<T, SIG>::kCtas;
 }
 
 template <class T>

@@ -48,8 +48,8 @@ __device__ __forceinline__ void write_part(const At& at, const f2 (&s)[At::P], f
 // Parameters, in order: W, P1 = gate w_post (a sigmoid gate is not in it), P0
 // = b_post (sigmoid gates only).
 template <class T, int V, int PER, int TEAM, int TOK, bool BRANCH, bool NORM, bool POST, bool SIG>
-__global__ void __launch_bounds__(bwd_threads<T, V, PER, TEAM, TOK, SIG>(),
-                                  bwd_ctas<T, V, PER, TEAM, TOK, SIG>())
+__global__ void __launch_bounds__(bwd_threads<T, V, PER, TEAM, SIG>(),
+                                  bwd_ctas<T, V, PER, TEAM, SIG>())
 sub_bwd_kernel(const __grid_constant__ SubArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   using At = Place<T, V, PER, TEAM, TOK, V == 1 ? kNarrowThreads : BwdSize<T, SIG>::kThreads>;
@@ -348,7 +348,7 @@ cudaError_t run_kernel(Kernel fn, const SubArgs& a, const SubShape& s, cudaStrea
 }
 template <class T, int V, int PER, int TEAM, int TOK, bool NORM, bool SIG>
 cudaError_t run_branch(const SubCall& c, const SubArgs& a, const SubShape& s, cudaStream_t st) {
-  if constexpr (NORM && !SIG)
+  if constexpr (NORM && !SIG && PER != kBwdWidePer && TEAM != kBig)
     if (!c.branch)
       return run_kernel(sub_bwd_kernel<T, V, PER, TEAM, TOK, false, true, false, false>, a, s, st);
   return c.post != LSH_NORM_NONE
@@ -361,17 +361,21 @@ cudaError_t run_branch(const SubCall& c, const SubArgs& a, const SubShape& s, cu
 template <class T, bool NORM, bool SIG>
 cudaError_t sub_bwd_type(const SubCall& c, const SubArgs& a, const SubShape& s, cudaStream_t st) {
   constexpr int V = 16 / (int)sizeof(T), TOK = BwdSize<T, SIG>::kTok;
-  if constexpr (NORM && !SIG) {
-    if (s.wide && s.per == kBwdWidePer)
-      return run_kernel(s.team == 32
-                            ? sub_bwd_kernel<T, V, kBwdWidePer, 32, 1, false, true, false, false>
-                            : sub_bwd_kernel<T, V, kBwdWidePer, 0, 1, false, true, false, false>,
-                        a, s, st);
+  if (s.wide && s.per == kBwdWidePer) {
+    if constexpr (NORM && !SIG)
+      if (!c.branch)
+        return run_kernel(s.team == 32
+                              ? sub_bwd_kernel<T, V, kBwdWidePer, 32, 1, false, true, false, false>
+                              : sub_bwd_kernel<T, V, kBwdWidePer, 0, 1, false, true, false, false>,
+                          a, s, st);
+    if constexpr (sizeof(T) == 2)
+      return run_branch<T, V, kBwdWidePer, 32, 1, NORM, SIG>(c, a, s, st);
   }
-  if (s.wide && s.tok < TOK) return run_branch<T, V, kBwdPer, 0, 1, NORM, SIG>(c, a, s, st);
+  if (s.wide && s.team > kBwdTeam)
+    return run_branch<T, V, kBwdPer, kBig, 1, NORM, SIG>(c, a, s, st);
   if (s.wide)
     return with_team(s.team, [&](auto t) {
-      return run_branch<T, V, kBwdPer, t.value, TOK, NORM, SIG>(c, a, s, st);
+      return run_branch<T, V, kBwdPer, t.value, t.value == 0 ? 1 : TOK, NORM, SIG>(c, a, s, st);
     });
   return s.team == 32 ? run_branch<T, 1, kNarrowPer, 32, 1, NORM, SIG>(c, a, s, st)
                       : run_branch<T, 1, kNarrowPer, 0, 1, NORM, SIG>(c, a, s, st);
