@@ -16,7 +16,7 @@ SubShape sub_shape(const SubCall& c, const SubSize& z) {
   s.wide = c.wide;
   for (const lsh_strides* t : {&c.sx, &c.sf, &c.sh})
     if ((c.H - 1) * t->h + c.d > (int64_t)INT32_MAX) s.wide = false;
-  int ctas, fixed;
+  int ctas, fixed, big = kFwdBig;
   for (;;) {
     const bool wide_rows = s.wide && z.backward && D > 32 * kBwdPer &&
                            (!c.branch || (c.dtype == LSH_BF16 && D <= kBwdWarpMax));
@@ -39,14 +39,15 @@ SubShape sub_shape(const SubCall& c, const SubSize& z) {
     // resident to cover their barriers (backward of 4 x 4096 tokens of 4096
     // features: 212 us against 245 with two)
     if (s.team > 32) s.tok = 1;
-    s.teams = std::max(1, threads / s.team);
+    const int cta = s.wide && !z.backward && s.team > 32 ? big : threads;
+    s.teams = std::max(1, cta / s.team);
     s.threads = s.teams * s.team;
     // threads resident on an SM, by the registers of each form
     int room = 512;
     if (wide_rows) room = kBwdRoom;
     else if (s.wide && z.backward && s.team > 32)
       room = s.team <= kBwdTeam ? kBwdTeamRoom : kBwdBigRoom;
-    else if (s.wide && (!z.backward || s.team <= 32)) room = z.ctas * threads;
+    else if (s.wide && s.team <= 32) room = z.ctas * threads;
     ctas = std::max(1, room / s.threads);
     fixed = z.vecs * per * 4 * s.team + (s.team > 32 ? s.teams * 64 * kMaxWarps : 0);
     s.stages = 1;
@@ -60,7 +61,8 @@ SubShape sub_shape(const SubCall& c, const SubSize& z) {
       if (all > kSms * ctas)
         while (ctas > 1 && fixed + 2 * stage > kSmemPerSm / ctas - 1024) --ctas;
       if (fixed + stage > kSmemPerSm / ctas - 1024) {
-        s.wide = false;
+        if (!z.backward && s.team > 32 && s.teams > 1) big = s.team;   // fewer teams first
+        else s.wide = false;
         continue;
       }
       s.stages = std::min(kMaxStages, (kSmemPerSm / ctas - 1024 - fixed) / stage);

@@ -554,6 +554,9 @@ cudaError_t with_team(int team, F f) {
 // 73 for 32K at 255 registers against 103 at 128, 2 x 256). A sigmoid gate's
 // kernel takes one token and 168 registers (114 us; 143 at 128, 127 at 255).
 constexpr int kFwdPer = 32, kFwdThreads = 256, kFwdCtas = 2, kFwdNormCtas = 3;
+// Teams of several warps, forward: one large CTA an SM, whose teams share the
+// parameters in shared memory (64 KB of them for 4096 features).
+constexpr int kFwdBig = 512;
 constexpr int kBwdPer = 16;
 constexpr int kNarrowThreads = 256;
 template <class T, bool SIG>

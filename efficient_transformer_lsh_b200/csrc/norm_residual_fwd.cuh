@@ -11,10 +11,10 @@ namespace {
 // B, P0 = gate b_post where there is one of them: the products are formed once
 // a CTA, not once a token.
 template <class T, int V, int PER, int TEAM, int TOK, bool BRANCH, bool POST, bool SIG>
-__global__ void __launch_bounds__(V == 1 ? 32 * kMaxWarps : kFwdThreads,
-                                  V == 1   ? 1
-                                  : BRANCH ? kFwdCtas
-                                           : kFwdNormCtas)
+__global__ void __launch_bounds__(V == 1 || TEAM == 0 ? kFwdBig : kFwdThreads,
+                                  V == 1 || TEAM == 0 ? 1
+                                  : BRANCH            ? kFwdCtas
+                                                      : kFwdNormCtas)
 sub_fwd_kernel(const __grid_constant__ SubArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   using At = Place<T, V, PER, TEAM, TOK, V == 1 ? kNarrowThreads : kFwdThreads>;
