@@ -107,14 +107,21 @@ SubArgs sub_args(const SubCall& c, const SubShape& s) {
   return a;
 }
 
+template <class T, bool BRANCH>
+static SubShape fwd_shape(const SubCall& c) {
+  using Z = FwdSize<T, BRANCH>;
+  return sub_shape(c, {kFwdPer, 1, Z::kThreads, 1 + BRANCH + (c.gate == LSH_GATE_SIGMOID),
+                       (BRANCH ? 2 : 1) * (c.b || c.bp ? 2 : 1), Z::kCtas, false});
+}
+
 cudaError_t launch_sub_fwd(const SubCall& c, cudaStream_t st) {
-  const SubShape s = sub_shape(c, {kFwdPer, 1, kFwdThreads,
-                                   1 + c.branch + (c.gate == LSH_GATE_SIGMOID),
-                                   (c.branch ? 2 : 1) * (c.b || c.bp ? 2 : 1),
-                                   c.branch ? kFwdCtas : kFwdNormCtas, false});
+  const bool bf16 = c.dtype == LSH_BF16;
+  const SubShape s = bf16 ? c.branch ? fwd_shape<__nv_bfloat16, true>(c)
+                                     : fwd_shape<__nv_bfloat16, false>(c)
+                     : c.branch ? fwd_shape<float, true>(c)
+                                : fwd_shape<float, false>(c);
   const SubArgs a = sub_args(c, s);
-  return c.dtype == LSH_BF16 ? sub_fwd_type<__nv_bfloat16>(c, a, s, st)
-                             : sub_fwd_type<float>(c, a, s, st);
+  return bf16 ? sub_fwd_type<__nv_bfloat16>(c, a, s, st) : sub_fwd_type<float>(c, a, s, st);
 }
 
 namespace {

@@ -553,7 +553,15 @@ cudaError_t with_team(int team, F f) {
 // registers, 2 x 128 threads an SM, 104 at 168, 3 x 128; float32 with one token
 // 73 for 32K at 255 registers against 103 at 128, 2 x 256). A sigmoid gate's
 // kernel takes one token and 168 registers (114 us; 143 at 128, 127 at 255).
-constexpr int kFwdPer = 32, kFwdThreads = 256, kFwdCtas = 2, kFwdNormCtas = 3;
+constexpr int kFwdPer = 32;
+template <class T, bool BRANCH>
+struct FwdSize {
+  // bf16 with a branch: four CTAs of 128 threads rather than two of 256 (64K
+  // tokens of 512 features 55 us, 58; the norm alone 32 us against 27)
+  static constexpr bool kSmall = BRANCH && sizeof(T) == 2;
+  static constexpr int kThreads = kSmall ? 128 : 256;
+  static constexpr int kCtas = kSmall ? 4 : BRANCH ? 2 : 3;
+};
 // Teams of several warps, forward: one large CTA an SM, whose teams share the
 // parameters in shared memory (64 KB of them for 4096 features).
 constexpr int kFwdBig = 512;

@@ -11,13 +11,11 @@ namespace {
 // B, P0 = gate b_post where there is one of them: the products are formed once
 // a CTA, not once a token.
 template <class T, int V, int PER, int TEAM, int TOK, bool BRANCH, bool POST, bool SIG>
-__global__ void __launch_bounds__(V == 1 || TEAM == 0 ? kFwdBig : kFwdThreads,
-                                  V == 1 || TEAM == 0 ? 1
-                                  : BRANCH            ? kFwdCtas
-                                                      : kFwdNormCtas)
+__global__ void __launch_bounds__(V == 1 || TEAM == 0 ? kFwdBig : FwdSize<T, BRANCH>::kThreads,
+                                  V == 1 || TEAM == 0 ? 1 : FwdSize<T, BRANCH>::kCtas)
 sub_fwd_kernel(const __grid_constant__ SubArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
-  using At = Place<T, V, PER, TEAM, TOK, V == 1 ? kNarrowThreads : kFwdThreads>;
+  using At = Place<T, V, PER, TEAM, TOK, V == 1 ? kNarrowThreads : FwdSize<T, BRANCH>::kThreads>;
   constexpr int P = At::P;
   At at(a, smem);
   stream_wait();
