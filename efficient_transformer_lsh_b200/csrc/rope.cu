@@ -11,6 +11,10 @@
 // or two heads it takes four or two tokens instead. bf16 takes the hardware's
 // approximate sine and cosine (absolute error below 2^-21 on one turn, where
 // a bf16 result is rounded at 2^-9 of its value), float32 the accurate ones.
+//
+// Bound by HBM: 33.5 M elements in bf16 take 23 us with 8 heads (134 MB, 5.8
+// TB/s), 67 M with 2 heads 44 us (6.0 TB/s); with one head the angles, one for
+// every two elements, still show (28.6 us).
 #include <algorithm>
 
 #include "internal.h"
@@ -197,6 +201,7 @@ cudaError_t run_order(const RopeArgs& a, bool inter, cudaStream_t s) {
 }
 
 // dx = (dqk turned back) + dv; a.in is dqk, float32 and contiguous like dv.
+// 33.5 M elements to bf16: 50.8 us (336 MB, 6.6 TB/s: HBM).
 template <class T, int P, bool INTER>
 __global__ void __launch_bounds__(kThreads)
 rope_sum_kernel(const __grid_constant__ RopeArgs a) {
