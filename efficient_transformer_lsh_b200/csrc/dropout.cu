@@ -43,7 +43,7 @@ template <class T, int V, int DIMS>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant__ DropArgs a) {
   stream_wait();
   let_next_start();
-  const uint64_t offset = a.offset + (a.counter ? __ldg(a.counter) : 0);
+  const uint64_t offset = a.offset + (a.counter ? *a.counter : 0);
   const int row0 = blockIdx.x * a.tile;
   const int n = min(a.tile, a.rows - row0) * (int)a.upr.d;
   for (int j0 = threadIdx.x; j0 < n; j0 += kThreads * kUnits) {

@@ -164,8 +164,8 @@ sub_final_kernel(const __grid_constant__ FinalArgs a) {
       const float* r = a.part + (int64_t)g * a.parts * row + v0 * a.D + c;
 #pragma unroll 8
       for (int p = i % lanes; p < a.parts; p += lanes) {
-        s1 += __ldcg(r + p * row);
-        s0 += __ldcg(r + p * row + a.D);
+        s1 += r[p * row];
+        s0 += r[p * row + a.D];
       }
     }
 #pragma unroll

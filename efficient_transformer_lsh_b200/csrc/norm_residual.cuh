@@ -386,9 +386,9 @@ struct Place {
       const int at = feat(4 * j / V) + 4 * j % V;
       const float x = zero ? 0.f : 1.f;
       float4 u = make_float4(x, x, x, x);
-      if (p) u = __ldg(reinterpret_cast<const float4*>(p + at));
+      if (p) u = *reinterpret_cast<const float4*>(p + at);
       if (q) {
-        const float4 w = __ldg(reinterpret_cast<const float4*>(q + at));
+        const float4 w = *reinterpret_cast<const float4*>(q + at);
         u = make_float4(u.x * w.x, u.y * w.y, u.z * w.z, u.w * w.w);
       }
       return on(4 * j / V) ? u : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -397,8 +397,8 @@ struct Place {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int k = 4 * j + i;
-        e[i] = p ? __ldg(p + feat(k)) : zero ? 0.f : 1.f;
-        if (q) e[i] *= __ldg(q + feat(k));
+        e[i] = p ? p[feat(k)] : zero ? 0.f : 1.f;
+        if (q) e[i] *= q[feat(k)];
         if (!on(k)) e[i] = 0.f;
       }
       return make_float4(e[0], e[1], e[2], e[3]);

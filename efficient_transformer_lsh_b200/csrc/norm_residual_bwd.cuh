@@ -70,7 +70,7 @@ sub_bwd_kernel(const __grid_constant__ SubArgs a) {
   const int i_dy = NORM ? 2 : 0, i_f = i_dy + (a.dy ? 1 : 0), i_z = i_f + 1;
   const int tensors = i_f + BRANCH + sig;
   if (at.on_bits != At::kAll) at.clear(at.ring, a.stages * tensors * TOK);
-  const uint64_t offset = a.offset + (a.counter ? __ldg(a.counter) : 0);
+  const uint64_t offset = a.offset + (a.counter ? *a.counter : 0);
   const int step = at.step(), rounds = at.rounds();
   const uint32_t one = at.one(), token_bytes = tensors * one, stage_bytes = TOK * token_bytes;
   const float own = at.count();

@@ -35,7 +35,7 @@ sub_fwd_kernel(const __grid_constant__ SubArgs a) {
   constexpr int kW = 0, kP1 = 1, kB = BRANCH ? 2 : 1, kP0 = 3;
   const int tensors = 1 + BRANCH + sig;
   if (at.on_bits != At::kAll) at.clear(at.ring, a.stages * tensors * TOK);
-  const uint64_t offset = a.offset + (a.counter ? __ldg(a.counter) : 0);
+  const uint64_t offset = a.offset + (a.counter ? *a.counter : 0);
   const int step = at.step(), rounds = at.rounds();
   const uint32_t one = at.one(), token_bytes = tensors * one, stage_bytes = TOK * token_bytes;
 

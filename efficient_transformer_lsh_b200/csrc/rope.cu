@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     out[i] = (T*)a.out + (b * a.so.b + l * a.so.l + c);
     pos[i] = a.pos0 + l;
     if (a.pos && t < a.tokens)
-      pos[i] = a.pos0 + __ldg(a.pos + (int64_t)b * a.pos_batch * a.L + l);
+      pos[i] = a.pos0 + a.pos[(int64_t)b * a.pos_batch * a.L + l];
   }
   Pairs<T, P, INTER> r[TB][HB];
   auto load = [&](int h) {
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   load(h0);   // on the way while the angles are formed
   uint64_t turns[P];
 #pragma unroll
-  for (int i = 0; i < P; ++i) turns[i] = pair ? __ldg(a.turns + u * P + i) : 0;
+  for (int i = 0; i < P; ++i) turns[i] = pair ? a.turns[u * P + i] : 0;
   float cs[TB == 1 ? P : 1], sn[TB == 1 ? P : 1];
   constexpr bool kFast = sizeof(T) == 2;
   if constexpr (TB == 1) {
@@ -221,10 +221,10 @@ rope_sum_kernel(const __grid_constant__ RopeArgs a) {
   float cs[P], sn[P];
   if (pair) {
     const int64_t pos =
-        a.pos0 + (a.pos ? (int64_t)__ldg(a.pos + (int64_t)b * a.pos_batch * a.L + l) : (int64_t)l);
+        a.pos0 + (a.pos ? (int64_t)a.pos[(int64_t)b * a.pos_batch * a.L + l] : (int64_t)l);
 #pragma unroll
     for (int i = 0; i < P; ++i)
-      angle<sizeof(T) == 2>(a, pos, __ldg(a.turns + u * P + i), cs[i], sn[i]);
+      angle<sizeof(T) == 2>(a, pos, a.turns[u * P + i], cs[i], sn[i]);
   }
   for (int h = h0; h < h1; h += HB) {
     Pairs<float, P, INTER> g[HB], v[HB];

@@ -11,7 +11,9 @@ namespace lsh {
 // Programmatic dependent launch: a kernel of this file's users lets the next
 // one of the stream be set up while it runs, and waits for all earlier work of
 // the stream before it touches memory. Every thread of every kernel waits, so
-// that the end of a kernel means the end of all before it.
+// that the end of a kernel means the end of all before it. All loads after the
+// wait are plain ones: a load that the compiler may take for one of constant
+// memory (ld.global.nc) could be moved before it.
 __device__ __forceinline__ void stream_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -108,24 +110,6 @@ struct Vec {
     }
   }
 };
-
-// V consecutive float32 parameters.
-template <int V>
-__device__ __forceinline__ void load_params(const float* p, float (&v)[V]) {
-  if constexpr (V % 4 == 0) {
-#pragma unroll
-    for (int i = 0; i < V / 4; ++i) {
-      const float4 u = __ldg(reinterpret_cast<const float4*>(p) + i);
-      v[4 * i] = u.x;
-      v[4 * i + 1] = u.y;
-      v[4 * i + 2] = u.z;
-      v[4 * i + 3] = u.w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = __ldg(p + i);
-  }
-}
 
 // n / d and n mod d for 0 <= n < 2^31 by one multiplication: with s =
 // ceil(log2 d) and m = ceil(2^(32+s) / d) - 2^32, (umulhi(n, m) + n) >> s is

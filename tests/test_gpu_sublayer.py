@@ -825,3 +825,71 @@ def test_reversible_layer_refuses():
         run.forward(x1, x2, R[:1], w)
     with pytest.raises(_lib.LshError):
         run.forward(x1, x2, R, w, offset=1 << 63)
+
+
+def test_a_call_reads_what_the_call_before_it_wrote():
+    """Launches overlap their set-up: parameters and activations that the
+    previous kernel of the stream wrote are those it wrote."""
+    from efficient_transformer_lsh_b200 import sublayer as sl
+    torch = _torch()
+    B, H, L = 1, 8, 6001
+    D = 64 * H
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rnd = lambda: torch.randn(B, H, L, 64, device="cuda", generator=g).bfloat16()
+    x, dh, f = rnd(), rnd(), rnd()
+    ones = torch.ones(D, device="cuda")
+    a, b = sl.Norm(B, H, L), sl.Norm(B, H, L)
+    r = sl.Residual(B, H, L, "rms", "layer", "vector", p=0.1)
+
+    def chain(wait):
+        out = []
+        for i in range(6):
+            dh.copy_(f).mul_(0.01 * (i + 1))
+            wait()
+            _, dw, db = a.backward(x, dh, ones, ones)          # dw, db are the next calls'
+            wait()
+            h = b.forward(x, dw, db)                           # parameters
+            wait()
+            y, h2 = r.forward(h, f, dw, db, None, dw, db, seed=i)
+            wait()
+            got = r.backward(h2, f, y, h, dw, db, None, dw, db, seed=i)
+            out += [t.clone() for t in (h, y, h2, *(t for t in got if t is not None))]
+        return out
+
+    want = chain(torch.cuda.synchronize)
+    for _ in range(3):
+        assert all(torch.equal(p, q) for p, q in zip(chain(lambda: None), want))
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    """No warm-up: the kernels are loaded while the graph is captured."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+from efficient_transformer_lsh_b200 import sublayer as sl
+B, H, L = 2, 5, 33
+x, f = (torch.randn(B, H, L, 64, device="cuda").bfloat16() for _ in range(2))
+w = torch.ones(64 * H, device="cuda")
+make = lambda: (sl.Residual(B, H, L, "rms", "layer", "vector", p=0.2), sl.Rotary(B, H, L),
+                sl.Dropout(B, H, L, 0.3))
+def step(r, e, d):
+    y, h = r.forward(x, f, w, w, None, w, w, seed=4)
+    return [y, h, e.forward(h), d.forward(h, 9)] + \\
+        [t for t in r.backward(f, f, y, x, w, w, None, w, w, seed=4) if t is not None]
+cap, eager = make(), make()
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    outs = step(*cap)
+graph.replay()
+want = step(*eager)
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(outs, want))
+print("captured")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
