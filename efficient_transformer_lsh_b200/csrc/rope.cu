@@ -42,22 +42,25 @@ struct RopeArgs {
   float amp, sign;
 };
 
-// P pairs of one unit: P low and P high features, or 2 P adjacent ones.
+// P pairs of one unit: P low and P high features, or 2 P adjacent ones in one
+// access. A single adjacent pair is two accesses, so that it needs no more
+// than its elements' alignment.
 template <class T, int P, bool INTER>
 struct Pairs {
-  Vec<T, INTER ? 2 * P : P> a;
-  Vec<T, INTER ? 1 : P> b;
+  static constexpr bool kJoined = INTER && P > 1;
+  Vec<T, kJoined ? 2 * P : P> a;
+  Vec<T, kJoined ? 1 : P> b;
   __device__ __forceinline__ void load(const T* p, int second) {
     a.load(p);
-    if constexpr (!INTER) b.load(p + second);
+    if constexpr (!kJoined) b.load(p + second);
   }
   __device__ __forceinline__ void store(T* p, int second) const {
     a.store(p);
-    if constexpr (!INTER) b.store(p + second);
+    if constexpr (!kJoined) b.store(p + second);
   }
   // firsts and seconds of the pairs (copied features: any split)
   __device__ __forceinline__ void get(float (&p)[P], float (&q)[P]) const {
-    if constexpr (INTER) {
+    if constexpr (kJoined) {
       float v[2 * P];
       a.get(v);
 #pragma unroll
@@ -68,7 +71,7 @@ struct Pairs {
     }
   }
   __device__ __forceinline__ void set(const float (&p)[P], const float (&q)[P]) {
-    if constexpr (INTER) {
+    if constexpr (kJoined) {
       float v[2 * P];
 #pragma unroll
       for (int i = 0; i < P; ++i) v[2 * i] = p[i], v[2 * i + 1] = q[i];
@@ -119,7 +122,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   // second: from a pair's first feature to its second (copies: the next P)
   const bool pair = u < a.pair_units;
   const int c = pair ? u * (INTER ? 2 * P : P) : a.rot + (u - a.pair_units) * 2 * P;
-  const int second = pair ? a.half : P;
+  const int second = pair && !INTER ? a.half : P;
   const int t0 = blockIdx.x * a.tile * TB + tt;
   const T* in[TB];
   T* out[TB];
@@ -214,7 +217,7 @@ rope_sum_kernel(const __grid_constant__ RopeArgs a) {
   const int h0 = blockIdx.y * a.heads, h1 = min(a.H, h0 + a.heads);
   const bool pair = u < a.pair_units;
   const int c = pair ? u * (INTER ? 2 * P : P) : a.rot + (u - a.pair_units) * 2 * P;
-  const int second = pair ? a.half : P;
+  const int second = pair && !INTER ? a.half : P;
   const int b = (int)a.fl.div((uint32_t)t), l = t - b * a.L;
   const int64_t from = b * a.si.b + l * a.si.l + c;
   T* out = (T*)a.out + (b * a.so.b + l * a.so.l + c);
