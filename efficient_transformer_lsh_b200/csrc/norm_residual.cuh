@@ -12,18 +12,18 @@
 // Every activation is read once and written once: a team of threads holds a
 // token's features in registers, PER a thread, and a row's sums are shuffles
 // (plus one exchange through shared memory per sum for teams of several
-// warps). What limits these kernels after HBM is the number of instructions:
-// teams are as small as registers allow (16 threads for 512 features), so
-// that addresses, shuffles and statistics, which cost the same for any team
-// of at most a warp, serve several tokens at once. Statistics take two passes over the registers (mean, then
-// squared deviations): one pass of sums of squares would lose what a mean far
-// from zero leaves.
+// warps). Statistics take two passes over the registers (mean, then squared
+// deviations): one pass of sums of squares would lose what a mean far from
+// zero leaves.
 //
-// What bounds them is HBM, if the loads of coming tokens are in flight while
-// a token is computed: each thread copies its own 16 features of each input
-// of the next tokens to a ring in shared memory (cp.async, 16 bytes a copy),
-// and reads them back itself, so the ring needs no barrier. Arithmetic runs
-// on pairs (fma.rn.f32x2 and its like): half the instructions.
+// The bound is HBM where the copies of coming tokens are in flight while a
+// token is computed: each thread copies its own features of each input of the
+// next tokens to a ring in shared memory (cp.async, 16 bytes a copy) and reads
+// them back itself, so the ring needs no barrier. After that it is the number
+// of instructions: arithmetic runs on pairs (fma.rn.f32x2 and its like), and
+// teams are as small as registers allow (16 threads for 512 features), so that
+// addresses, shuffles and statistics, which cost the same for any team of at
+// most a warp, serve several tokens at once.
 #pragma once
 
 #include <algorithm>
@@ -379,13 +379,11 @@ struct Place {
   }
 
   // ---- parameters ----
-  // Features 4 j .. 4 j + 3 of the thread of p times q (absent: ones, or
-  // zeros where `zero`); 0 past D.
-  __device__ __forceinline__ float4 param4(const float* p, const float* q, bool zero, int j) const {
+  // Features 4 j .. 4 j + 3 of the thread of p times q (absent: ones); 0 past D.
+  __device__ __forceinline__ float4 param4(const float* p, const float* q, int j) const {
     if constexpr (kRing) {
       const int at = feat(4 * j / V) + 4 * j % V;
-      const float x = zero ? 0.f : 1.f;
-      float4 u = make_float4(x, x, x, x);
+      float4 u = make_float4(1.f, 1.f, 1.f, 1.f);
       if (p) u = *reinterpret_cast<const float4*>(p + at);
       if (q) {
         const float4 w = *reinterpret_cast<const float4*>(q + at);
@@ -397,7 +395,7 @@ struct Place {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int k = 4 * j + i;
-        e[i] = p ? p[feat(k)] : zero ? 0.f : 1.f;
+        e[i] = p ? p[feat(k)] : 1.f;
         if (q) e[i] *= q[feat(k)];
         if (!on(k)) e[i] = 0.f;
       }
@@ -405,11 +403,10 @@ struct Place {
     }
   }
   // Parameters sit in shared memory as [vector][PER / 4][team] groups of four.
-  __device__ __forceinline__ void stage_param(int vec, const float* p, const float* q,
-                                              bool zero = false) const {
+  __device__ __forceinline__ void stage_param(int vec, const float* p, const float* q) const {
     // the teams of the CTA share the groups out
     for (int j = team_id; j < PER / 4; j += a.teams) {
-      const float4 u = param4(p, q, zero, j);
+      const float4 u = param4(p, q, j);
       sts16(par + (vec * (PER / 4) + j) * team() * 16,
             make_uint4(__float_as_uint(u.x), __float_as_uint(u.y), __float_as_uint(u.z),
                        __float_as_uint(u.w)));
@@ -534,7 +531,6 @@ SubArgs sub_args(const SubCall& c, const SubShape& s);
 template <class F>
 cudaError_t with_team(int team, F f) {
   switch (team) {
-    case 1:
     case 2: return f(std::integral_constant<int, 2>());
     case 4: return f(std::integral_constant<int, 4>());
     case 8: return f(std::integral_constant<int, 8>());

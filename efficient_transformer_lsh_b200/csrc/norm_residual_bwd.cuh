@@ -73,7 +73,7 @@ sub_bwd_kernel(const __grid_constant__ SubArgs a) {
   const uint64_t offset = a.offset + (a.counter ? *a.counter : 0);
   const int step = at.step(), rounds = at.rounds();
   const uint32_t one = at.one(), token_bytes = tensors * one, stage_bytes = TOK * token_bytes;
-  const float own = at.count();
+  const float own = at.count(), inv_own = own > 0.f ? 1.f / own : 0.f;
   const bool lf = post && a.post == LSH_NORM_LAYER, ly = NORM && a.norm == LSH_NORM_LAYER;
   f2 sa[P], sb[P], s1[P], s0[P];
 #pragma unroll
@@ -162,7 +162,7 @@ sub_bwd_kernel(const __grid_constant__ SubArgs a) {
           if (lf) {
             get_f(a.f, i_f, j, q[j]);
             s[2 * j + 1] = sum_all(q[j]);
-            own_mean[j] = at.on_bits ? s[2 * j + 1] / own : 0.f;
+            own_mean[j] = s[2 * j + 1] * inv_own;
             at.center(q[j], own_mean[j]);
             own_sq[j] = dot_all(q[j], q[j]);
           }
