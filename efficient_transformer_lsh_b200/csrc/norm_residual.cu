@@ -15,7 +15,9 @@ SubShape sub_shape(const SubCall& c, const SubSize& z) {
   s.tokens = c.gate_batch ? c.L : c.B * c.L;
   s.wide = c.wide;
   for (const lsh_strides* t : {&c.sx, &c.sf, &c.sh})
-    if ((c.H - 1) * t->h + c.d > (int64_t)INT32_MAX) s.wide = false;
+    if ((c.H - 1) * t->h + c.d > (int64_t)INT32_MAX ||
+        std::max(t->b, t->l) / (16 / esize) > (int64_t)UINT32_MAX)
+      s.wide = false;
   int ctas, fixed, big = kFwdBig;
   for (;;) {
     const bool wide_rows = s.wide && z.backward && D > 32 * kBwdPer &&
@@ -90,7 +92,10 @@ SubArgs sub_args(const SubCall& c, const SubShape& s) {
   a.wp = c.wp, a.bp = c.bp, a.w = c.w, a.b = c.b;
   a.z = c.gate == LSH_GATE_SIGMOID ? c.gatep : nullptr;
   a.gv = c.gate == LSH_GATE_VECTOR ? (const float*)c.gatep : nullptr;
-  a.sx = c.sx, a.sf = c.sf, a.sh = c.sh;
+  const auto layout = [V](const lsh_strides& t) {
+    return SubLayout{t, (uint32_t)(t.b / V), (uint32_t)(t.l / V)};
+  };
+  a.sx = layout(c.sx), a.sf = layout(c.sf), a.sh = layout(c.sh);
   a.upr = FastDiv((uint32_t)(c.d / V));
   a.fl = FastDiv((uint32_t)std::max(1, c.L));
   a.H = c.H, a.L = c.L, a.D = c.H * c.d;

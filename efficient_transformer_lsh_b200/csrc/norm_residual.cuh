@@ -42,12 +42,19 @@ constexpr int kSms = 148;
 constexpr int kSmemPerSm = 226 * 1024;
 constexpr int kSmemDefault = 48 * 1024;   // of a CTA without asking for more
 
+// Strides in elements and, for the kernels that move vectors of 16 bytes, of
+// batch and token in such vectors: 32-bit factors of one multiplication each.
+struct SubLayout {
+  lsh_strides s;
+  uint32_t b, l;
+};
+
 struct SubArgs {
   const void *x, *f, *z, *dy, *dh;
   void *y, *h, *dx, *df, *dz;
   const float *wp, *bp, *gv, *w, *b;
   float* part;
-  lsh_strides sx, sf, sh;
+  SubLayout sx, sf, sh;
   FastDiv upr, fl;        // vectors of a head row; L
   int H, L, D, units, gpr;
   int tokens, parts;      // tokens of a group; CTAs of a group
@@ -180,7 +187,7 @@ struct Place {
   static constexpr uint32_t kAll = (uint32_t)((1ull << NV) - 1);
   const SubArgs& a;
   int group, part, team_id, lane;   // lane: thread of the team
-  int ox[kKeep], of[kKeep], oh[kKeep];   // a vector's place in a token, by strides
+  int ox[kKeep], of[kKeep], oh[kKeep];   // a vector's place in a token, in vectors
   uint32_t on_bits, ring, par;
   float* red;
   int turn = 0;
@@ -197,9 +204,9 @@ struct Place {
     if constexpr (kRing) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        ox[k] = (int)place(a.sx, k);
-        of[k] = (int)place(a.sf, k);
-        oh[k] = (int)place(a.sh, k);
+        ox[k] = (int)(place(a.sx, k) / V);
+        of[k] = (int)(place(a.sf, k) / V);
+        oh[k] = (int)(place(a.sh, k) / V);
       }
     }
     par = (uint32_t)__cvta_generic_to_shared(smem) + lane * 16;
@@ -221,8 +228,8 @@ struct Place {
   __device__ __forceinline__ int col(int k) const {
     return (unit(k) - head(k) * (int)a.upr.d) * V;
   }
-  __device__ __forceinline__ int64_t place(const lsh_strides& s, int k) const {
-    return head(k) * s.h + col(k);
+  __device__ __forceinline__ int64_t place(const SubLayout& s, int k) const {
+    return head(k) * s.s.h + col(k);
   }
 
   // ---- tokens ----
@@ -243,8 +250,10 @@ struct Place {
       l = t - b * a.L;
     }
   }
-  static __device__ __forceinline__ int64_t row(const lsh_strides& s, int b, int l) {
-    return b * s.b + l * s.l;
+  // a token's place: in vectors for the ring's kernels, else in elements
+  static __device__ __forceinline__ int64_t row(const SubLayout& s, int b, int l) {
+    if constexpr (kRing) return (int64_t)((uint64_t)(uint32_t)b * s.b + (uint64_t)(uint32_t)l * s.l);
+    return b * s.s.b + l * s.s.l;
   }
 
   // Sums of N values over the team, the same on each of its threads. Several
@@ -308,13 +317,13 @@ struct Place {
   }
   __device__ __forceinline__ void issue(const void* p, const int (&o)[kKeep], int64_t row,
                                         uint32_t at) const {
-    const T* q = (const T*)p + row;
+    const uint4* q = (const uint4*)p + row;
 #pragma unroll
     for (int k = 0; k < NV; ++k)
       if (on(k)) cp_async16(at + k * slot(), q + o[k]);
   }
   // `at`: the tensor's slots of this stage; V = 1: from memory.
-  __device__ __forceinline__ void get(const void* p, const lsh_strides& s, int b, int l, bool live,
+  __device__ __forceinline__ void get(const void* p, const SubLayout& s, int b, int l, bool live,
                                       uint32_t at, f2 (&v)[P]) const {
     if constexpr (kRing) {
 #pragma unroll
@@ -351,9 +360,9 @@ struct Place {
   // ---- outputs ----
   // Stores v; with BACK v becomes what was stored.
   template <bool BACK>
-  __device__ __forceinline__ void put(void* p, const lsh_strides& s, const int (&o)[kKeep],
+  __device__ __forceinline__ void put(void* p, const SubLayout& s, const int (&o)[kKeep],
                                       int b, int l, bool live, f2 (&v)[P]) const {
-    T* q = (T*)p + row(s, b, l);
+    T* q = kRing ? (T*)((uint4*)p + row(s, b, l)) : (T*)p + row(s, b, l);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       float e[V];
@@ -364,7 +373,8 @@ struct Place {
       }
       Vec<T, V> r;
       r.set(e);
-      if (live && on(k)) r.store(q + (kRing ? o[kRing ? k : 0] : place(s, k)));
+      if (live && on(k))
+        r.store(kRing ? (T*)((uint4*)q + o[kRing ? k : 0]) : q + place(s, k));
       if (BACK && sizeof(T) == 2) {
         r.get(e);
         if constexpr (kRing) {
@@ -514,8 +524,8 @@ __device__ __forceinline__ float inv_std(float sum_sq, float inv_d, float eps) {
 
 // How a problem is laid over the GPU, with `ctas` CTAs of an SM resident where
 // two ring stages of each fit, else fewer. `wide` goes by room and reach too:
-// one stage has to fit, and a token's vectors have to lie within 2^31 elements
-// of its first.
+// one stage has to fit, a token's vectors have to lie within 2^31 elements of
+// its first, and strides below 2^32 vectors.
 struct SubShape {
   int per, team, teams, threads, tok, groups, tokens, parts, stages, vecs, smem;
   bool wide;

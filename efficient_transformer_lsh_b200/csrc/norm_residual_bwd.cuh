@@ -115,7 +115,8 @@ sub_bwd_kernel(const __grid_constant__ SubArgs a) {
     }
   };
   // the first tokens are on the way while the parameters are staged
-  for (int i = 1; i < a.stages; ++i) copy();
+  const bool ahead = a.stages > 1;
+  for (int i = ahead; i < a.stages; ++i) copy();
   if (NORM) at.stage_param(0, a.w, nullptr);
   if (has1) at.stage_param(kP1, a.wp, gv);
   if (has0) at.stage_param(kP0, a.bp, nullptr);
@@ -123,7 +124,7 @@ sub_bwd_kernel(const __grid_constant__ SubArgs a) {
   uint32_t st = at.ring;
   int t = at.first();
   for (int n = 0; n < rounds; ++n, t += step) {
-    copy();
+    if (n > 0 || ahead) copy();
     if constexpr (At::kRing) cp_wait_for(a.stages - 1);
     int b[TOK], l[TOK];
     bool live[TOK];

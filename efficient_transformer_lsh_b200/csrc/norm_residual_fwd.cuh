@@ -67,7 +67,8 @@ sub_fwd_kernel(const __grid_constant__ SubArgs a) {
     }
   };
   // the first tokens are on the way while the parameters are staged
-  for (int i = 0; i < a.stages; ++i) copy();
+  const bool ahead = a.stages > 1;
+  for (int i = ahead; i < a.stages; ++i) copy();
   if (norm && (a.w || a.b)) at.stage_param(kW, a.w, nullptr);
   if (has1 || has0) at.stage_param(kP1, a.wp, gv);
   if (norm && a.b) at.stage_param(kB, a.b, nullptr);
@@ -76,6 +77,7 @@ sub_fwd_kernel(const __grid_constant__ SubArgs a) {
   uint32_t st = at.ring;
   int t = at.first();
   for (int n = 0; n < rounds; ++n, t += step) {
+    if (n > 0 || ahead) copy();
     if constexpr (At::kRing) cp_wait_for(a.stages - 1);
     int b[TOK], l[TOK];
     bool live[TOK];
@@ -84,7 +86,7 @@ sub_fwd_kernel(const __grid_constant__ SubArgs a) {
       live[j] = (At::kMulti && TOK == 1) || t + j < a.tokens;
       at.token(t + j, b[j], l[j]);
     }
-    auto get = [&](const void* p, const lsh_strides& s, int i, int j, f2(&v)[P]) {
+    auto get = [&](const void* p, const SubLayout& s, int i, int j, f2(&v)[P]) {
       at.get(p, s, b[j], l[j], live[j], st + j * token_bytes + i * one, v);
     };
     f2 v[TOK][P];
@@ -151,7 +153,6 @@ sub_fwd_kernel(const __grid_constant__ SubArgs a) {
     }
     st += stage_bytes;
     if (st == at.ring + a.stages * stage_bytes) st = at.ring;
-    copy();
   }
   if constexpr (At::kRing) cp_wait<0>();
 }
