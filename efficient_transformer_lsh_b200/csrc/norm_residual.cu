@@ -39,7 +39,7 @@ SubShape sub_shape(const SubCall& c, const SubSize& z) {
     }
     // Teams of several warps take one token at a time, with more of them
     // resident to cover their barriers (backward of 4 x 4096 tokens of 4096
-    // features: 212 us against 245 with two)
+    // features: 212 us, where two tokens took 245)
     if (s.team > 32) s.tok = 1;
     const int cta = s.wide && !z.backward && s.team > 32 ? big : threads;
     s.teams = std::max(1, cta / s.team);

@@ -555,15 +555,16 @@ cudaError_t with_team(int team, F f) {
 // two tokens of 512. Backward: the four sums of parameter gradients already
 // take four registers a feature, so 16 features, and a few warps with all the
 // registers they can use, rather than more that spill (64K tokens of 512
-// features with everything on: bf16 with two tokens at a time 100 us at 255
-// registers, 2 x 128 threads an SM, 104 at 168, 3 x 128; float32 with one token
-// 73 for 32K at 255 registers against 103 at 128, 2 x 256). A sigmoid gate's
-// kernel takes one token and 168 registers (114 us; 143 at 128, 127 at 255).
+// features with everything on: bf16 with two tokens at a time 94 us at 255
+// registers, 2 x 128 threads an SM, 109 at 168, 3 x 128; float32 with one token
+// 75 for 32K at 255 registers, 80 at 168, 98 at 128). A sigmoid gate's kernel
+// takes one token and 168 registers (111 us; 133 at 128, 118 at 255).
 constexpr int kFwdPer = 32;
 template <class T, bool BRANCH>
 struct FwdSize {
   // bf16 with a branch: four CTAs of 128 threads rather than two of 256 (64K
-  // tokens of 512 features 55 us, 58; the norm alone 32 us against 27)
+  // tokens of 512 features 52.9 us, 56; float32 prefers the two: 32K
+  // tokens 49.8 us, 52.7 with three of 128)
   static constexpr bool kSmall = BRANCH && sizeof(T) == 2;
   static constexpr int kThreads = kSmall ? 128 : 256;
   static constexpr int kCtas = kSmall ? 4 : BRANCH ? 2 : 3;
@@ -583,10 +584,10 @@ struct BwdSize {
 // Rows wider than 512 features in the backward. A norm's own (two sums a
 // feature, not four) holds 32 features a thread at any width, and so does
 // bf16 with a branch up to 1024, where that makes a warp of a token (2 x 12288
-// tokens of 1024 features: 77 us; 98 with two warps of 16 features a thread).
+// tokens of 1024 features: 75 us; 96 with two warps of 16 features a thread).
 // Wider ones take several warps of 16: 168 registers up to 192 threads, else
-// 128 for two CTAs an SM (12288 tokens of 2048 features: 106 us at 168, 116 at
-// 128; 16384 of 4096: 264 and 212).
+// 128 for two teams an SM (12288 tokens of 2048 features: 96 us at 168, 117 at
+// 128; 16384 of 4096: 200 with two teams, 241 with one at 255).
 constexpr int kBwdWidePer = 32, kBwdWarpMax = 1024;
 constexpr int kBwdRoom = 256;                           // threads an SM at 255 registers
 constexpr int kBwdTeam = 192, kBwdTeamRoom = 384;       // at 168

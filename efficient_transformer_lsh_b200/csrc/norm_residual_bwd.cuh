@@ -16,12 +16,12 @@
 // statistics, so r is factored out: mean(a yhat) = r mean(a (y - mean))); then
 // the second norm's a and a (f - mean).
 //
-// 64K tokens of 512 features in bf16: a norm's 50.2 us with the sum of the
-// partials (268 MB, 5.3 TB/s); with everything on 97.4 us (403 MB, 4.1 TB/s),
-// bound by its instructions (about 810 a token and warp, of which 130 are the
-// dropout's) at the two warps a scheduler that 234 registers leave (three of
+// 64K tokens of 512 features in bf16: a norm's 49.8 us with the sum of the
+// partials (268 MB, 5.4 TB/s); with everything on 93.8 us (403 MB, 4.3 TB/s),
+// bound by its instructions (about 765 a token and warp, of which 130 are the
+// dropout's) at the two warps a scheduler that 230 registers leave (three of
 // 168 registers spill: 102.7 us where this was 100.3). float32: a norm
-// of 64K tokens 92 us, 5.8 TB/s (HBM).
+// of 64K tokens 93 us, 5.8 TB/s (HBM).
 #pragma once
 
 #include "norm_residual.cuh"

@@ -9,11 +9,11 @@ namespace {
 
 // One pass: the row of f (or x) in registers, its statistics, the gate, the
 // dropout, the add, y's statistics and h, each activation read and written
-// once. 64K tokens of 512 features: a norm alone 26.7 us (134 MB, 5.0 TB/s),
-// with everything on 54.8 us (268 MB, 4.9 TB/s); there the instructions of a
+// once. 64K tokens of 512 features: a norm alone 25.9 us (134 MB, 5.2 TB/s),
+// with everything on 52.9 us (268 MB, 5.1 TB/s); there the instructions of a
 // token (about 520 a warp) take as long as its bytes: bf16 unpacking, the two
 // statistics, ten Philox rounds for every 8 features. 4 x 8192 tokens of 4096
-// features, a norm: 85 us (537 MB, 6.3 TB/s: HBM).
+// features, a norm: 82 us (537 MB, 6.5 TB/s: HBM).
 //
 // Parameters, in order: W, P1 = gate w_post (a sigmoid gate is not in it), then
 // B, P0 = gate b_post where there is one of them: the products are formed once
