@@ -139,29 +139,32 @@ struct FinalArgs {
   float *dgate, *dwp, *dbp, *dw, *db;
 };
 
-// Adds the CTAs' rows, in a fixed order. Block (x, y): 8 features (one sector),
-// y = 0 the norm's pair, y = 1 the branch's; 64 threads a feature add rows i,
-// i + 64, ... of a group, all loads in flight, then a warp's four, then the
-// warps in order. (32 features and 32 threads each: 9.2 us for 444 rows of 512
-// features, the latency of two rounds of loads on 16 SMs.)
-constexpr int kFinalCols = 8, kFinalRows = 64, kFinalWarps = kFinalCols * kFinalRows / 32;
-__global__ void __launch_bounds__(kFinalCols* kFinalRows)
+// Adds the CTAs' rows, in a fixed order. Block (x, y): COLS features, y = 0 the
+// norm's pair, y = 1 the branch's; R = 512 / COLS threads a feature add rows i,
+// i + R, ... of a group, all loads in flight, then a warp's, then the warps in
+// order. 8 features (one sector) below 2048, so that there are blocks for the
+// SMs (444 rows of 512 features: 9.2 us with 32); 32 from there, where 8 make
+// several waves of blocks of a few loads each.
+constexpr int kFinalThreads = 512, kFinalWarps = kFinalThreads / 32, kFinalWide = 2048;
+template <int COLS>
+__global__ void __launch_bounds__(kFinalThreads)
 sub_final_kernel(const __grid_constant__ FinalArgs a) {
-  __shared__ float buf[2][kFinalWarps][kFinalCols];
+  __shared__ float buf[2][kFinalWarps][COLS];
+  constexpr int kRows = kFinalThreads / COLS;
   stream_wait();
   let_next_start();
-  const int col = threadIdx.x % kFinalCols, i = threadIdx.x / kFinalCols;
+  const int col = threadIdx.x % COLS, i = threadIdx.x / COLS;
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c = blockIdx.x * kFinalCols + col;
+  const int c = blockIdx.x * COLS + col;
   const bool on = c < a.D;
   const bool branch = a.norm ? blockIdx.y == 1 : true;
   const int v0 = branch && a.norm ? 2 : 0;
   const int64_t row = (int64_t)a.vecs * a.D;
-  // Few groups: one after the other, 64 threads a feature each. Many (a gate
+  // Few groups: one after the other, kRows threads a feature each. Many (a gate
   // for each of 16 sequences or more): a warp takes every 16th group, which
   // has few rows then, with four threads a feature.
   const bool many = a.groups >= kFinalWarps;
-  const int lanes = many ? kFinalRows / kFinalWarps : kFinalRows;
+  const int lanes = many ? kRows / kFinalWarps : kRows;
   float t1 = 0.f, t0 = 0.f;   // totals over the groups
   for (int g = many ? w : 0; g < a.groups; g += many ? kFinalWarps : 1) {
     float s1 = 0.f, s0 = 0.f;
@@ -174,13 +177,13 @@ sub_final_kernel(const __grid_constant__ FinalArgs a) {
       }
     }
 #pragma unroll
-    for (int o = kFinalCols; o < 32; o <<= 1) {
+    for (int o = COLS; o < 32; o <<= 1) {
       s1 += __shfl_xor_sync(0xffffffffu, s1, o);
       s0 += __shfl_xor_sync(0xffffffffu, s0, o);
     }
     if (!many) {
       __syncthreads();
-      if (lane < kFinalCols) {
+      if (lane < COLS) {
         buf[0][w][col] = s1;
         buf[1][w][col] = s0;
       }
@@ -194,7 +197,7 @@ sub_final_kernel(const __grid_constant__ FinalArgs a) {
     }
     if (branch && on) {
       const float gate = a.gv ? a.gv[(a.gate_batch ? (int64_t)g * a.D : 0) + c] : 1.f;
-      if (a.dgate && lane < kFinalCols && (many || w == 0))
+      if (a.dgate && lane < COLS && (many || w == 0))
         a.dgate[(int64_t)g * a.D + c] =
             (a.wp ? a.wp[c] : 1.f) * s1 + (a.bp ? a.bp[c] * s0 : 0.f);
       t1 = fmaf(gate, s1, t1);
@@ -206,7 +209,7 @@ sub_final_kernel(const __grid_constant__ FinalArgs a) {
   }
   if (many) {
     __syncthreads();
-    if (lane < kFinalCols) {
+    if (lane < COLS) {
       buf[0][w][col] = t1;
       buf[1][w][col] = t0;
     }
@@ -278,10 +281,11 @@ cudaError_t launch_sub_bwd(const SubCall& c, void* ws, cudaStream_t st) {
   f.wp = c.wp, f.bp = c.bp, f.gv = a.gv, f.gate_batch = c.gate_batch;
   f.dgate = c.dgate, f.dwp = c.dwp, f.dbp = c.dbp, f.dw = c.dw, f.db = c.db;
   note_launch();
-  return launch_overlapped(sub_final_kernel,
-                           dim3((unsigned)((a.D + kFinalCols - 1) / kFinalCols),
+  const int cols = a.D < kFinalWide ? 8 : 32;
+  return launch_overlapped(cols == 8 ? sub_final_kernel<8> : sub_final_kernel<32>,
+                           dim3((unsigned)((a.D + cols - 1) / cols),
                                 (unsigned)(f.norm + f.branch)),
-                           kFinalCols * kFinalRows, 0, st, f);
+                           kFinalThreads, 0, st, f);
 }
 
 }  // namespace lsh

@@ -282,8 +282,12 @@ struct Place {
       }
 #pragma unroll
       for (int o = W / N / 2; o > 0; o >>= 1) x[0] += __shfl_xor_sync(all, x[0], o);
+      if constexpr (kMulti) {
+        v[0] = x[0];   // lane i W / N has value i
+      } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = __shfl_sync(all, x[0], i * (W / N), W);
+        for (int i = 0; i < N; ++i) v[i] = __shfl_sync(all, x[0], i * (W / N), W);
+      }
     } else {
 #pragma unroll
       for (int o = W / 2; o > 0; o >>= 1)
@@ -294,16 +298,28 @@ struct Place {
       float* r = red + turn * (8 * kMaxWarps);
       turn ^= 1;
       const int nw = a.team >> 5;
-      if ((lane & 31) == 0) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) r[i * kMaxWarps + (lane >> 5)] = v[i];
-      }
+      if ((me & (W / N - 1)) == 0) r[(lane >> 5) * N + me / (W / N)] = v[0];
       asm volatile("bar.sync %0, %1;" ::"r"(team_id + 1), "r"(a.team) : "memory");
+      // the warps' values in order, two at a time where there are two
+      if constexpr (N == 1) {
+        v[0] = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < nw; ++k) v[0] += r[k];
+      } else {
+        f2 s[N / 2];
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        float s = 0.f;
-        for (int k = 0; k < nw; ++k) s += r[i * kMaxWarps + k];
-        v[i] = s;
+        for (int i = 0; i < N / 2; ++i) s[i] = 0ull;
+#pragma unroll 4
+        for (int k = 0; k < nw; ++k)
+#pragma unroll
+          for (int i = 0; i < N / 2; ++i)
+            s[i] = add2(s[i], *reinterpret_cast<const f2*>(r + k * N + 2 * i));
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+          const float2 u = up(s[i]);
+          v[2 * i] = u.x;
+          v[2 * i + 1] = u.y;
+        }
       }
     }
   }
