@@ -21,7 +21,10 @@ SubShape sub_shape(const SubCall& c, const SubSize& z) {
   int ctas, fixed, big = kFwdBig;
   for (;;) {
     const bool wide_rows = s.wide && z.backward && D > 32 * kBwdPer &&
-                           (!c.branch || (c.dtype == LSH_BF16 && D <= kBwdWarpMax));
+                           (!c.branch ||
+                            (c.dtype == LSH_BF16 &&
+                             (D <= kBwdWarpMax ||
+                              (c.gate != LSH_GATE_SIGMOID && D > kBwdTeam * kBwdPer))));
     const int per = !s.wide ? kNarrowPer : wide_rows ? kBwdWidePer : z.per;
     const int threads = s.wide ? z.threads : kNarrowThreads;
     s.per = per;
@@ -57,11 +60,15 @@ SubShape sub_shape(const SubCall& c, const SubSize& z) {
     if (s.wide) {
       const int stage = z.tensors * s.tok * (s.team > 32 ? s.threads : threads) * per * esize;
       // two stages before more CTAs, unless that many CTAs have no second
-      // round to copy ahead for
+      // round to copy ahead for; but one stage before a single CTA of a
+      // backward with barriers, which another one covers (8192 tokens of 4096
+      // features in float32: 306 us with one CTA, 208 with two; 3 CTAs of one
+      // stage for 12288 of 1536: 95, 80 with two)
       const int64_t all = ((int64_t)s.tokens + s.teams * s.tok - 1) / (s.teams * s.tok) * s.groups;
       while (ctas > 1 && fixed + stage > kSmemPerSm / ctas - 1024) --ctas;
+      const int least = z.backward && s.team > 32 ? 2 : 1;
       if (all > kSms * ctas)
-        while (ctas > 1 && fixed + 2 * stage > kSmemPerSm / ctas - 1024) --ctas;
+        while (ctas > least && fixed + 2 * stage > kSmemPerSm / ctas - 1024) --ctas;
       if (fixed + stage > kSmemPerSm / ctas - 1024) {
         if (!z.backward && s.team > 32 && s.teams > 1) big = s.team;   // fewer teams first
         else s.wide = false;

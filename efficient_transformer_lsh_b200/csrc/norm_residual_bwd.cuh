@@ -390,11 +390,14 @@ cudaError_t sub_bwd_type(const SubCall& c, const SubArgs& a, const SubShape& s, 
                               ? sub_bwd_kernel<T, V, kBwdWidePer, 32, 1, false, true, false, false>
                               : sub_bwd_kernel<T, V, kBwdWidePer, 0, 1, false, true, false, false>,
                           a, s, st);
+    if constexpr (sizeof(T) == 2 && !SIG)
+      if (s.team > 32) return run_branch<T, V, kBwdWidePer, 0, 1, NORM, SIG>(c, a, s, st);
     if constexpr (sizeof(T) == 2)
       return run_branch<T, V, kBwdWidePer, 32, 1, NORM, SIG>(c, a, s, st);
   }
-  if (s.wide && s.team > kBwdTeam)
-    return run_branch<T, V, kBwdPer, kBig, 1, NORM, SIG>(c, a, s, st);
+  if constexpr (sizeof(T) == 4 || SIG)
+    if (s.wide && s.team > kBwdTeam)
+      return run_branch<T, V, kBwdPer, kBig, 1, NORM, SIG>(c, a, s, st);
   if (s.wide)
     return with_team(s.team, [&](auto t) {
       return run_branch<T, V, kBwdPer, t.value, t.value == 0 ? 1 : TOK, NORM, SIG>(c, a, s, st);
