@@ -176,6 +176,16 @@ RES_CASES = [
     (100, 2, 3, 64, "bf16", "layer", "rms", "vector", True, 0.1, 1.0, 1.0, "head", "head", 0),
     (17, 1, 40, 64, "f32", None, "layer", "vector", True, 0.0, 1.0, 1.0, "head", "head", 0),
     (16, 9, 1, 64, "bf16", "rms", None, "vector", True, 0.0, 1.0, 1.0, "token", "token", 0),
+    # wide rows: teams of several warps with several rounds, each form of the backward
+    (1, 64, 700, 64, "bf16", "layer", "layer", "vector", False, 0.1, 0.5, 1.0, "head", "token", 0),
+    (1, 49, 350, 64, "bf16", "rms", None, None, False, 0.0, 1.0, 1.0, "token", "head", 0),
+    (1, 128, 320, 64, "bf16", "layer", "rms", None, False, 0.1, 1.0, 0.5, "head", "head", 0),
+    (1, 64, 640, 64, "bf16", "layer", "layer", "sigmoid", False, 0.1, 1.0, 1.0, "head", "head", 0),
+    (1, 64, 640, 64, "f32", "rms", "layer", "vector", False, 0.1, 1.0, 1.0, "token", "token", 0),
+    (2, 32, 450, 64, "bf16", "layer", None, "sigmoid", False, 0.0, 1.0, 1.0, "head", "head", 0),
+    # parameter gradients of wide rows whose last block of features is not full
+    (1, 33, 333, 72, "bf16", "layer", "layer", "vector", False, 0.1, 1.0, 1.0, "head", "head", 0),
+    (17, 33, 3, 72, "f32", "layer", "layer", "vector", True, 0.1, 1.0, 1.0, "head", "head", 0),
 ]
 
 
