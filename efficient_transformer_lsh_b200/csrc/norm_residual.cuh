@@ -601,9 +601,12 @@ struct BwdSize {
 // feature, not four) holds 32 features a thread at any width, and so does
 // bf16 with a branch up to 1024, where that makes a warp of a token (2 x 12288
 // tokens of 1024 features: 75 us; 96 with two warps of 16 features a thread).
-// Wider ones take several warps of 16: 168 registers up to 192 threads, else
-// 128 for two teams an SM (12288 tokens of 2048 features: 96 us at 168, 117 at
-// 128; 16384 of 4096: 200 with two teams, 241 with one at 255).
+// Wider ones take several warps of 16: 168 registers up to 192 threads (12288
+// tokens of 2048 features: 80 us; 92 with 32 features a thread, 100 at 128
+// registers). Past that, bf16 has 32 features a thread again (8192 tokens of
+// 4096: 125 us; 143 with 16 at 128 registers), float32 and sigmoid gates 16 at
+// 128 registers for two teams an SM (with 32, before there were two: float32
+// as fast, a sigmoid gate's 344 us where this was 302).
 constexpr int kBwdWidePer = 32, kBwdWarpMax = 1024;
 constexpr int kBwdRoom = 256;                           // threads an SM at 255 registers
 constexpr int kBwdTeam = 192, kBwdTeamRoom = 384;       // at 168
