@@ -10,7 +10,8 @@ strides are those of the driver's layout:
 
   "head"           [B, H, L, d] contiguous (the attention's layout);
   "token"          [B, L, H, d] contiguous, seen as [B, H, L, d];
-  (sb, sh, sl)     any strides in elements, features adjacent.
+  (sb, sh, sl)     any strides in elements, features adjacent; positive where
+                   the dimension is longer than 1, elements distinct.
 
 A tensor of another shape, type, device or layout raises ``LshError`` before
 anything is launched. Parameters and their gradients are float32, contiguous.
@@ -68,7 +69,12 @@ class _Driver:
             return (H * L * d, d, H * d, 1)
         if isinstance(layout, str) or len(layout) != 3:
             _refuse(type(self).__name__, f"layout {layout!r}")
-        return tuple(int(s) for s in layout) + (1,)
+        strides = tuple(int(s) for s in layout)
+        # all zero would say "contiguous" to the library
+        if not self._empty and any(n > 1 and s < 1 for n, s in zip(self.shape, strides)):
+            _refuse(type(self).__name__, f"layout {layout!r}: strides of dimensions longer than "
+                                         "1 are positive")
+        return strides + (1,)
 
     def _buffer(self, strides) -> torch.Tensor:
         """An activation buffer of the driver's own in the layout's order."""
@@ -79,6 +85,7 @@ class _Driver:
             return torch.empty(self.shape, dtype=self.tdtype, device=self.device)
         if self._empty:
             return torch.empty(self.shape, dtype=self.tdtype, device=self.device)
+        strides = [max(0, s) for s in strides]   # below 0: of a single element
         last = sum((n - 1) * s for n, s in zip(self.shape, strides))
         return torch.empty(last + 1, dtype=self.tdtype, device=self.device).as_strided(
             self.shape, strides)
