@@ -16,7 +16,8 @@ strides are those of the driver's layout:
 A tensor of another shape, type, device or layout raises ``LshError`` before
 anything is launched. Parameters and their gradients are float32, contiguous.
 Work is queued on ``stream`` (default: the current stream of the driver's
-device).
+device). A driver made for another device than a GPU describes its problem, but
+refuses its calls.
 """
 from __future__ import annotations
 
@@ -128,7 +129,11 @@ class _Driver:
             return method(*args, **kw)
 
     def _stream(self, stream):
-        """Handle of a stream; None is the device's current one."""
+        """Handle of a stream; None is the device's current one. The last thing
+        that every call looks up, so a driver of host memory, whose addresses no
+        kernel can take, ends here."""
+        if self._index < 0:
+            _refuse(type(self).__name__, f"made for {self.device}, its calls need a CUDA device")
         if stream is None:
             return _current_stream(self._index)
         return stream if isinstance(stream, int) else stream.cuda_stream

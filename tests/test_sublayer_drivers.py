@@ -36,3 +36,29 @@ def test_strides_of_single_elements_say_nothing(sl):
     assert sl.Norm(1, 1, 1, x_layout=(0, 0, 0), **CPU).dx.shape == (1, 1, 1, 64)
     assert sl.Norm(1, 2, 1, x_layout=(0, 64, -5), **CPU).dx.shape == (1, 2, 1, 64)
     assert sl.Dropout(2, 0, 3, 0.1, x_layout=(0, 0, 0), **CPU).y.numel() == 0
+
+
+def test_host_memory_is_refused_by_every_call(sl):
+    """A driver of a device that no kernel runs on is refused with the argument
+    error, not by whatever a launch on host addresses does."""
+    import torch
+    x = torch.zeros(1, 2, 3, 64, dtype=torch.bfloat16)
+    w, pos = torch.ones(128), torch.zeros(3, dtype=torch.int32)
+    f32 = x.float()
+    n, d, e = sl.Norm(1, 2, 3, **CPU), sl.Dropout(1, 2, 3, 0.1, **CPU), sl.Rotary(1, 2, 3, **CPU)
+    r, q = sl.Residual(1, 2, 3, norm="rms", **CPU), sl.Residual(1, 2, 3, **CPU)
+    lay = sl.ReversibleLayer(1, 2, 128, 2, 1, 64, True, 256, 128, norm="rms", rot=0, **CPU)
+    z = torch.zeros(1, 2, 128, 64, dtype=torch.bfloat16)
+    R = torch.zeros(1, 64, 1, dtype=torch.bfloat16)
+    p = dict(W1=torch.zeros(128, 256).bfloat16(), W2=torch.zeros(256, 128).bfloat16(),
+             b1=torch.zeros(256), b2=torch.zeros(128), norm1_w=w, norm2_w=w)
+    for call in (lambda: n.forward(x, w, w), lambda: n.backward(x, x, w, w, x),
+                 lambda: n.forward(x, stream=0), lambda: d.forward(x, 1),
+                 lambda: d.backward(x, 1), lambda: e.forward(x, pos), lambda: e.backward(x),
+                 lambda: e.backward_sum(f32, f32), lambda: r.forward(x, x, w=w),
+                 lambda: r.restore(x, x), lambda: r.backward(None, x, x, x),
+                 lambda: q.forward(x, x), lambda: q.backward(x, x),
+                 lambda: lay.forward(z, z, R, p), lambda: lay.backward(z, z, z, z, p)):
+        with pytest.raises(_lib.LshError) as err:
+            call()
+        assert err.value.code == 1
