@@ -33,6 +33,7 @@ _TORCH_DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16}
 _KINDS = {None: _lib.LSH_NORM_NONE, "layer": _lib.LSH_NORM_LAYER, "rms": _lib.LSH_NORM_RMS}
 _GATES = {None: _lib.LSH_GATE_NONE, "vector": _lib.LSH_GATE_VECTOR,
           "sigmoid": _lib.LSH_GATE_SIGMOID}
+_INT32_MAX = (1 << 31) - 1   # the C structs' sizes
 Layout = Union[str, Sequence[int]]
 _current_device = getattr(torch._C, "_cuda_getDevice", lambda: -1)
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0)
@@ -51,6 +52,8 @@ class _Driver:
         self.B, self.H, self.L, self.d = int(B), int(H), int(L), int(d)
         if min(self.B, self.H, self.L) < 0 or self.d < 1:
             _refuse(type(self).__name__, "sizes must not be negative")
+        if max(self.B, self.H, self.L, self.d) > _INT32_MAX:
+            _refuse(type(self).__name__, "sizes are below 2^31")
         self.dtype = dtype
         self.tdtype = _TORCH_DTYPE[dtype]
         self.shape = (self.B, self.H, self.L, self.d)
@@ -151,6 +154,12 @@ class _Driver:
         return torch.empty(max(1, n), dtype=torch.uint8, device=self.device)
 
 
+def _slice0(v, name):
+    if not 0 <= int(v) <= _INT32_MAX:
+        _refuse(name, f"slice0 {v}")
+    return int(v)
+
+
 def _seed(v, name):
     if v.__class__ is not int:
         v = int(v)
@@ -223,6 +232,7 @@ class Dropout(_Driver):
     def __init__(self, B, H, L, p, dtype="bf16", d=64, x_layout: Layout = "head",
                  y_layout: Layout = "head", slice0=0, device="cuda"):
         super().__init__(B, H, L, d, dtype, device)
+        slice0 = _slice0(slice0, "Dropout")
         self.sx, self.sy = self._strides(x_layout), self._strides(y_layout)
         self.p = _lib.make_dropout_problem(B, H, L, d, dtype, p, slice0, self.sx[:3], self.sy[:3])
         self.p_bwd = _lib.make_dropout_problem(B, H, L, d, dtype, p, slice0, self.sy[:3],
@@ -266,6 +276,7 @@ class Residual(_Driver):
         if post not in _KINDS or norm not in _KINDS or gate not in _GATES:
             _refuse("Residual", f"post {post!r}, norm {norm!r}, gate {gate!r}")
         self.post, self.norm, self.gate = post, norm, gate
+        slice0 = _slice0(slice0, "Residual")
         self.sx, self.sf = self._strides(x_layout), self._strides(f_layout)
 
         def problem(norm, alpha, beta):

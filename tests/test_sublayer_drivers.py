@@ -62,3 +62,26 @@ def test_host_memory_is_refused_by_every_call(sl):
         with pytest.raises(_lib.LshError) as err:
             call()
         assert err.value.code == 1
+
+
+@pytest.mark.parametrize("dims", [((1 << 32) + 1, 1, 0), (1, (1 << 32) + 1, 0),
+                                  (0, 1, (1 << 32) + 1), (1 << 31, 1, 0)])
+def test_sizes_past_32_bits_are_refused(sl, dims):
+    """The C structs hold 32-bit sizes: a larger one would be cut to another
+    problem. (Empty problems, so that no buffer of that size is made.)"""
+    for make in (lambda: sl.Norm(*dims, d=1, **CPU), lambda: sl.Residual(*dims, d=1, **CPU),
+                 lambda: sl.Dropout(*dims, 0.1, d=1, **CPU),
+                 lambda: sl.Rotary(*dims, d=2, **CPU)):
+        with pytest.raises(_lib.LshError):
+            make()
+    with pytest.raises(_lib.LshError):
+        sl.Dropout(1, 1, 0, 0.1, d=(1 << 32) + 8, **CPU)
+
+
+@pytest.mark.parametrize("slice0", [-1, 1 << 31, 1 << 64, (1 << 64) + 3])
+def test_slices_past_32_bits_are_refused(sl, slice0):
+    """2^64 + 3 would be cut to slice 3, and draw its mask."""
+    with pytest.raises(_lib.LshError):
+        sl.Dropout(1, 2, 3, 0.1, slice0=slice0, **CPU)
+    with pytest.raises(_lib.LshError):
+        sl.Residual(1, 2, 3, p=0.1, slice0=slice0, **CPU)
