@@ -559,7 +559,11 @@ class ReversibleLayer(_Driver):
         self.dW2 = torch.empty((self.d_ff, self.D), **f32)
         self.db2 = torch.empty((self.D,), **f32)
 
-    def _check(self, w):
+    def _check(self, w, acts, seed, counter):
+        """All that the calls of a step would refuse, before the first of them."""
+        head = self._strides("head")
+        for name, t in acts.items():
+            self._act(t, head, name)
         want = {"W1", "b1", "W2", "b2"}
         for i in "12":
             want |= {f"norm{i}_w"} | ({f"norm{i}_b"} if self.norm == "layer" else set())
@@ -569,11 +573,18 @@ class ReversibleLayer(_Driver):
                 want.add(f"gate{i}")
         if set(w) != want:
             _refuse("ReversibleLayer", f"parameters {sorted(w)}, expected {sorted(want)}")
-        bf16 = torch.bfloat16
-        self._vec(w["W1"], (self.D, self.d_ff), "W1", bf16)
-        self._vec(w["W2"], (self.d_ff, self.D), "W2", bf16)
-        self._vec(w["b1"], (self.d_ff,), "b1")
-        self._vec(w["b2"], (self.D,), "b2")
+        bf16, f32 = torch.bfloat16, torch.float32
+        ff = dict(W1=((self.D, self.d_ff), bf16), b1=((self.d_ff,), f32),
+                  W2=((self.d_ff, self.D), bf16), b2=((self.D,), f32))
+        for name in want:
+            shape, dtype = ff.get(name, ((self.D,), f32))
+            at = self._vec(w[name], shape, name, dtype)
+            if at is None and (name in ff or name[:4] == "gate"):
+                _refuse("ReversibleLayer", f"{name} is missing")
+            if name in ff and at % 16:
+                _refuse("ReversibleLayer", f"{name}: its address is not a multiple of 16")
+        _seed(seed, "ReversibleLayer")
+        self._vec(counter, (1,), "counter", torch.int64)
 
     def _offsets(self, offset):
         if not 0 <= int(offset) < 1 << 63:
@@ -605,11 +616,11 @@ class ReversibleLayer(_Driver):
         sequence has position pos0 + l."""
         if self._away():
             return self._there(self.forward, x1, x2, R, w, seed, offset, counter, pos0, stream)
-        self._check(w)
+        self._check(w, dict(x1=x1, x2=x2), seed, counter)
         o1, o2 = self._offsets(offset)
-        head = self._strides("head")
-        self._act(x1, head, "x1"), self._act(x2, head, "x2")
         p = self.attn.p
+        if R is None:
+            _refuse("ReversibleLayer", "R is missing")
         self._vec(R, (p.n_rounds, 64, p.n_buckets // 2), "R", torch.bfloat16)
         _, _, f = self._attend(x2, w, pos0, stream, R)
         rng = dict(seed=seed, counter=counter, stream=stream)
@@ -626,7 +637,7 @@ class ReversibleLayer(_Driver):
         if self._away():
             return self._there(self.backward, y1, y2, dy1, dy2, w, seed, offset, counter, pos0,
                                stream)
-        self._check(w)
+        self._check(w, dict(y1=y1, y2=y2, dy1=dy1, dy2=dy2), seed, counter)
         o1, o2 = self._offsets(offset)
         rng = dict(seed=seed, counter=counter, stream=stream)
         b1, b2 = self._branch(w, 1), self._branch(w, 2)

@@ -1,0 +1,52 @@
+"""Further calls of the operators around a sublayer: what a refused call leaves
+alone, far positions, both ways of a stride's reach, arrays that are input and
+output at once. Tolerances as in test_gpu_sublayer, with fewer roundings where
+fewer are made."""
+import numpy as np
+import pytest
+
+import test_gpu_sublayer as base
+from oracle import sublayer_oracle as orc
+
+pytestmark = pytest.mark.gpu
+U = base.U
+
+
+def test_a_refused_call_of_the_layer_launches_nothing():
+    """A refusal halfway would have replaced the permutation that the backward
+    of the forward before it needs."""
+    from efficient_transformer_lsh_b200 import _lib
+    torch = base._torch()
+    run, w, _, acts, R = base._layer("rms", True, "layer", 64, 0.1, True, 1)
+    x1, x2, dy1, dy2 = (a[0] for a in acts)
+    y1, y2 = (t.clone() for t in run.forward(x1, x2, R, w, seed=3))
+    torch.cuda.synchronize()
+    perm = run.attn.perm.clone()
+    short = torch.ones(64, device="cuda")
+    wrong = [{**w, k: short} for k in ("norm1_w", "norm1_b", "norm2_w", "norm2_b", "post1_w",
+                                       "post2_w", "gate1", "gate2", "b2")]
+    wrong.append({**w, "norm2_w": w["norm2_w"].bfloat16()})
+    wrong += [{**w, k: None} for k in ("W1", "b1", "W2", "b2", "gate1", "gate2")]
+    for k in ("W1", "b1", "W2", "b2"):     # the products read 16 bytes at once
+        room = torch.zeros(w[k].numel() + 1, dtype=w[k].dtype, device="cuda")
+        wrong.append({**w, k: room[1:].view(w[k].shape)})
+    int32 = torch.zeros(1, dtype=torch.int32, device="cuda")
+    calls = [lambda p=p: run.forward(x2, x1, R, p, seed=3) for p in wrong]
+    calls += [lambda p=p: run.backward(y1, y2, dy1, dy2, p, seed=3) for p in wrong]
+    for kw in (dict(seed=-1), dict(seed=1 << 64), dict(counter=int32), dict(offset=-1),
+               dict(counter=torch.zeros(1, dtype=torch.int64))):
+        calls.append(lambda kw=kw: run.forward(x2, x1, R, w, **kw))
+        calls.append(lambda kw=kw: run.backward(y1, y2, dy1, dy2, w, **kw))
+    for i in range(4):
+        t = [y1, y2, dy1, dy2]
+        t[i] = t[i].float()
+        calls.append(lambda t=t: run.backward(*t, w, seed=3))
+    calls += [lambda: run.forward(x2.float(), x1, R, w), lambda: run.forward(x2, x1[:1], R, w),
+              lambda: run.forward(x2, x1, R.float(), w), lambda: run.forward(x2, x1, None, w)]
+    before = _lib.lsh_launch_count()
+    for i, call in enumerate(calls):
+        with pytest.raises(_lib.LshError):
+            call()
+        assert _lib.lsh_launch_count() == before, i
+    torch.cuda.synchronize()
+    assert torch.equal(run.attn.perm, perm)
