@@ -2,15 +2,16 @@
 //
 // The angle is formed as a phase in turns, by the integer product position *
 // turns modulo 2^64 (turns = freq / 2 pi as a 64-bit fraction): the integer
-// wrap is the reduction modulo one turn, exact at any distance, where a
-// float32 product of position and frequency would lose the phase (0.03 rad
-// at position 2^20). Its top 32 bits, signed, are half turns in [-1, 1).
+// wrap is the reduction modulo one turn, exact, so that only the table's
+// rounding grows with the position (2^-65 of a turn each), where a float32
+// product of position and frequency would lose the phase (0.03 rad at position
+// 2^20). Its top 32 bits, signed, are half turns in [-1, 1).
 //
 // Sine and cosine of a (token, pair) serve every head: a thread keeps those
 // of its pairs in registers and walks the heads, four rows in flight; with one
 // or two heads it takes four or two tokens instead. bf16 takes the hardware's
 // approximate sine and cosine (absolute error below 2^-21 on one turn, where
-// a bf16 result is rounded at 2^-9 of its value), float32 the accurate ones.
+// a bf16 result is rounded at 2^-8 of its value), float32 the accurate ones.
 //
 // Bound by HBM: 33.5 M elements in bf16 take 23 us with 8 heads (134 MB, 5.8
 // TB/s), 67 M with 2 heads 44 us (6.0 TB/s); with one head the angles, one for

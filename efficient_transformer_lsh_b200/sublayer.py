@@ -22,6 +22,7 @@ refuses its calls.
 from __future__ import annotations
 
 import ctypes
+import decimal
 import math
 from typing import Optional, Sequence, Tuple, Union
 
@@ -387,6 +388,44 @@ class Residual(_Driver):
         return self.dx, self.df, self.dgate, dw_post, db_post, dw, db
 
 
+# Frequencies and tables are formed with 60 digits: a phase is off by the
+# position times the table's error, so a double's 53 bits would show from
+# position 2^31 on.
+_DIGITS = decimal.Context(prec=60)
+_TWO_PI = decimal.Decimal("6.28318530717958647692528676655900576839433879875021164194989")
+
+
+def _frequencies(rot, base, scaling):
+    """``rope_frequencies`` as decimals."""
+    rot, base = int(rot), float(base)
+    if rot < 2 or rot % 2:
+        _refuse("rope_frequencies", f"rot {rot}")
+    if not (base > 0 and math.isfinite(base)):
+        _refuse("rope_frequencies", f"base {base}")
+    kind = None if scaling is None else scaling[0]
+    if kind not in (None, "linear", "ntk", "yarn") or \
+            (kind and (len(scaling) != (3 if kind == "yarn" else 2) or
+                       not all(0 < v < math.inf for v in scaling[1:]))) or \
+            (kind == "ntk" and rot == 2):
+        _refuse("rope_frequencies", f"scaling {scaling!r}")
+    with decimal.localcontext(_DIGITS):
+        D = decimal.Decimal
+        amp, b = 1.0, D(base)
+        s = D(float(scaling[1])) if kind else D(1)
+        if kind == "ntk":
+            b *= s ** (D(rot) / (rot - 2))
+        f = [b ** (D(-2 * i) / rot) for i in range(rot // 2)]
+        if kind == "linear":
+            f = [v / s for v in f]
+        elif kind == "yarn":
+            turns = D(float(scaling[2])) / _TWO_PI
+            for i, v in enumerate(f):
+                keep = min(D(1), max(D(0), (turns * v - 1) / 31))
+                f[i] = v * keep + v / s * (1 - keep)
+            amp = 0.1 * math.log(float(scaling[1])) + 1.0
+        return f, amp
+
+
 def rope_frequencies(rot, base=10000.0, scaling=None):
     """(frequencies, amp): radians a position of the rot / 2 pairs, base^(-2i /
     rot), and the multiplier of the turned features. scaling for contexts
@@ -399,39 +438,23 @@ def rope_frequencies(rot, base=10000.0, scaling=None):
                           length L0 keep their frequency, those that turn less
                           than once are divided by s, a linear ramp between;
                           amp = 0.1 ln s + 1 (Peng et al. 2023)."""
-    rot = int(rot)
-    if rot < 2 or rot % 2:
-        _refuse("rope_frequencies", f"rot {rot}")
-    base, amp = float(base), 1.0
-    kind = None if scaling is None else scaling[0]
-    if kind not in (None, "linear", "ntk", "yarn") or \
-            (kind and (len(scaling) != (3 if kind == "yarn" else 2) or scaling[1] <= 0)) or \
-            (kind == "yarn" and scaling[2] <= 0) or (kind == "ntk" and rot == 2):
-        _refuse("rope_frequencies", f"scaling {scaling!r}")
-    if kind == "ntk":
-        base *= float(scaling[1]) ** (rot / (rot - 2))
-    f = [base ** (-2.0 * i / rot) for i in range(rot // 2)]
-    if kind == "linear":
-        f = [v / scaling[1] for v in f]
-    elif kind == "yarn":
-        s, L0 = float(scaling[1]), float(scaling[2])
-        for i, v in enumerate(f):
-            keep = min(1.0, max(0.0, (L0 * v / (2 * math.pi) - 1.0) / 31.0))
-            f[i] = v * keep + v / s * (1.0 - keep)
-        amp = 0.1 * math.log(s) + 1.0
-    return f, amp
+    f, amp = _frequencies(rot, base, scaling)
+    return [float(v) for v in f], amp
 
 
 def rope_turns(frequencies) -> torch.Tensor:
-    """Frequencies (radians a position) as 64-bit fractions of a turn, the bits
-    of an unsigned number in an int64 tensor (what ``lsh_rope_fwd`` reads)."""
+    """Frequencies (radians a position; floats, or decimals) as 64-bit fractions
+    of a turn, to the nearest: the bits of an unsigned number in an int64 tensor
+    (what ``lsh_rope_fwd`` reads)."""
     out = []
-    for f in frequencies:
-        t = f / (2.0 * math.pi)
-        if not math.isfinite(t):
-            _refuse("rope_turns", f"frequency {f}")
-        n = int(math.ldexp(t - math.floor(t), 64)) & ((1 << 64) - 1)
-        out.append(n - (1 << 64) if n >> 63 else n)
+    with decimal.localcontext(_DIGITS):
+        for f in frequencies:
+            v = f if isinstance(f, decimal.Decimal) else decimal.Decimal(float(f))
+            if not v.is_finite():
+                _refuse("rope_turns", f"frequency {f}")
+            t = v / _TWO_PI
+            n = int(((t - t.to_integral_value()) * (1 << 64)).to_integral_value()) % (1 << 64)
+            out.append(n - (1 << 64) if n >> 63 else n)
     return torch.tensor(out, dtype=torch.int64)
 
 
@@ -449,7 +472,7 @@ class Rotary(_Driver):
         if self.rot < 2 or self.rot % 2 or self.rot > self.d:
             _refuse("Rotary", f"rot {rot} of {d}")
         if frequencies is None:
-            frequencies, a = rope_frequencies(self.rot, base, scaling)
+            frequencies, a = _frequencies(self.rot, base, scaling)
             amp = a if amp is None else amp
         if len(frequencies) != self.rot // 2:
             _refuse("Rotary", f"{len(frequencies)} frequencies for rot {self.rot}")

@@ -385,9 +385,10 @@ lsh_status lsh_residual_bwd(const lsh_residual_problem* q, const void* dy, const
  *   turn in pairs, (2i, 2i+1) when interleaved, else (i, i + rot/2), by the
  *   angle position * freq_i: (p, q) -> amp (p cos - q sin, q cos + p sin);
  *   the other d - rot features are copied. turns[i] (device, uint64[rot/2])
- *   is freq_i / (2 pi) modulo 1 as a 64-bit fraction, so that position *
- *   turns[i] modulo 2^64 is the exact phase at any distance: an angle formed
- *   in float32 is off by 0.03 at position 2^20. Position scalings for long
+ *   is freq_i / (2 pi) modulo 1 as a 64-bit fraction. position * turns[i]
+ *   modulo 2^64 is exact, so the phase is off by position * the table's error
+ *   alone, 2^-65 of a turn where it is rounded from more bits: 2^-25 at position
+ *   2^40, where an angle formed in float32 is off by 0.03 at 2^20. Position scalings for long
  *   contexts are choices of turns and amp.
  *   Position of token (b, l): pos0 + (pos ? pos[b pos_batch L + l] : l), any
  *   sign.

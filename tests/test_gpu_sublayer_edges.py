@@ -50,3 +50,31 @@ def test_a_refused_call_of_the_layer_launches_nothing():
         assert _lib.lsh_launch_count() == before, i
     torch.cuda.synchronize()
     assert torch.equal(run.attn.perm, perm)
+
+
+@pytest.mark.parametrize("dtype,inter,scale", [("f32", False, 1), ("f32", True, 4),
+                                               ("bf16", False, 1)])
+def test_rope_at_far_positions(dtype, inter, scale):
+    """Phases from integers: position * frequency / 2 pi modulo 1, of which the
+    table holds 64 bits, so that it adds |position| 2^-65 turns: at 2^40 2 pi
+    2^-25 of angle, below 4 roundings, to the 8 and 21 of test_rope."""
+    from efficient_transformer_lsh_b200 import sublayer as sl
+    from test_sublayer_drivers import exact_turns
+    torch = base._torch()
+    B, H, L, d = 1, 2, 5, 64
+    shape, pos0 = (B, H, L, d), (1 << 40) - 3
+    g = np.random.default_rng(scale)
+    x, x64 = base._put(g.standard_normal(shape), dtype)
+    r = sl.Rotary(B, H, L, interleaved=inter, dtype=dtype,
+                  scaling=("linear", scale) if scale > 1 else None)
+    y = r.forward(x, pos0=pos0)
+    turns = [t / scale for t in exact_turns()]
+    k = 25 if dtype == "bf16" else 12
+    for l in range(L):
+        angle = np.array([float((pos0 + l) * t % 1) * 2 * np.pi for t in turns])
+        row = x64[:, :, l:l + 1]
+        want = orc.rope(row, angle, [1], d, inter)
+        base._close(y[:, :, l:l + 1], want, dtype, base._pair_sum(np.abs(row), d, inter), k)
+    back = r.backward(y, pos0=pos0).double().cpu().numpy()
+    assert np.abs(back - x64).max() < 2.0 ** -5
+    assert torch.isfinite(y).all()

@@ -85,3 +85,51 @@ def test_slices_past_32_bits_are_refused(sl, slice0):
         sl.Dropout(1, 2, 3, 0.1, slice0=slice0, **CPU)
     with pytest.raises(_lib.LshError):
         sl.Residual(1, 2, 3, p=0.1, slice0=slice0, **CPU)
+
+
+def _pi(bits):
+    """floor(pi 2^bits) by Machin's formula, 16 atan(1/5) - 4 atan(1/239)."""
+    def atan_inv(n):
+        one = 1 << (bits + 32)
+        total, term, k, sign = 0, one // n, 1, 1
+        while term:
+            total += sign * (term // k)
+            term //= n * n
+            k, sign = k + 2, -sign
+        return total
+    return (16 * atan_inv(5) - 4 * atan_inv(239)) >> 32
+
+
+def exact_turns():
+    """10000^(-2i/64) / 2 pi as fractions right to 100 bits: 10^(-i/8) is three
+    integer square roots."""
+    from fractions import Fraction
+    from math import isqrt
+    pi, out = Fraction(_pi(250), 1 << 250), []
+    for i in range(32):
+        root = isqrt(isqrt(isqrt(10 ** (8 * 60 - i))))
+        out.append(Fraction(root, 10 ** 60) / (2 * pi))
+    return out
+
+
+def test_rope_tables_hold_64_bits(sl):
+    """Within half a unit of 2^-64, which is |position| 2^-65 turns of phase."""
+    from fractions import Fraction
+    half = Fraction(1, 2) + Fraction(1, 1000)
+    off = lambda n, t: abs((int(n) % (1 << 64) - t % 1 * (1 << 64) + (1 << 63)) % (1 << 64)
+                           - (1 << 63))
+    for scale in (1, 8):
+        e = sl.Rotary(1, 1, 1, scaling=("linear", scale) if scale > 1 else None, **CPU)
+        for n, t in zip(e.turns, exact_turns()):
+            assert off(n, t / scale) <= half
+    # given frequencies are what their doubles say
+    pi = Fraction(_pi(250), 1 << 250)
+    fs = [1.0, 0.1, 3.0e-5, 6.5, -0.25, 1e9 + 0.5, 0.0]
+    for n, f in zip(sl.rope_turns(fs), fs):
+        assert off(n, Fraction(f) / (2 * pi)) <= half
+    for bad in (float("nan"), float("inf")):
+        with pytest.raises(_lib.LshError):
+            sl.rope_turns([bad])
+    for base in (0.0, -2.0, float("inf")):
+        with pytest.raises(_lib.LshError):
+            sl.rope_frequencies(64, base)
