@@ -283,7 +283,7 @@ sub_bwd_kernel(const __grid_constant__ SubArgs a) {
           for (int i = 0; i < P; ++i) {
             const float2 w = up(z[i]);
             float d0, d1;
-            const float g0 = sigmoid(w.x, d0), g1 = sigmoid(w.y, d1);
+            const float g0 = sigmoid<T>(w.x, d0), g1 = sigmoid<T>(w.y, d1);
             u[0][i] = mul2(u[0][i], mul2(q[j][i], pk(d0, d1)));
             q[j][i] = mul2(q[j][i], pk(g0, g1));
           }

@@ -121,7 +121,7 @@ sub_fwd_kernel(const __grid_constant__ SubArgs a) {
           for (int i = 0; i < P; ++i) {
             const float2 u = up(z[i]);
             float slope;
-            const float g0 = sigmoid(u.x, slope), g1 = sigmoid(u.y, slope);
+            const float g0 = sigmoid<T>(u.x, slope), g1 = sigmoid<T>(u.y, slope);
             v[j][i] = mul2(v[j][i], pk(g0, g1));
           }
         }

@@ -78,3 +78,27 @@ def test_rope_at_far_positions(dtype, inter, scale):
     back = r.backward(y, pos0=pos0).double().cpu().numpy()
     assert np.abs(back - x64).max() < 2.0 ** -5
     assert torch.isfinite(y).all()
+
+
+def test_sigmoid_gate_over_its_range_in_float32():
+    """Relative to the value at every z. Exponential 2 units (4 roundings of
+    2^-24), 1 + e half a unit, the quotient 2 units: gate at most 4 + (1 + 2 +
+    4) + 1 = 12 roundings (the exponential's error enters 1 + e by at most
+    half), slope 4 + 2 * 7 + 2 = 20; and two or three products."""
+    from efficient_transformer_lsh_b200 import sublayer as sl
+    B, H, L, d = 1, 2, 80, 64
+    shape = (B, H, L, d)
+    g = np.random.default_rng(4)
+    num = lambda: base._put(g.uniform(0.5, 2.0, shape) * g.choice([-1.0, 1.0], shape), "f32")
+    f, f64 = num()
+    dy, dy64 = num()
+    z, z64 = base._put(np.linspace(-80.0, 80.0, f64.size).reshape(shape), "f32")
+    x, _ = base._put(np.zeros(shape), "f32")
+    r = sl.Residual(B, H, L, gate="sigmoid", dtype="f32")
+    y, _ = r.forward(x, f, z)
+    s, t = (1 / (1 + np.exp(-v)) for v in (z64, -z64))
+    base._close(y, s * f64, "f32", np.abs(s * f64), 13)
+    _, df, dz = r.backward(dy, f, gate=z)[:3]
+    base._close(df, s * dy64, "f32", np.abs(s * dy64), 13)
+    want = dy64 * f64 * s * t
+    base._close(dz, want, "f32", np.abs(want), 23)
