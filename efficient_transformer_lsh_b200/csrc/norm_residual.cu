@@ -15,7 +15,7 @@ SubShape sub_shape(const SubCall& c, const SubSize& z) {
   s.tokens = c.gate_batch ? c.L : c.B * c.L;
   s.wide = c.wide;
   for (const lsh_strides* t : {&c.sx, &c.sf, &c.sh})
-    if ((c.H - 1) * t->h + c.d > (int64_t)INT32_MAX ||
+    if (((c.H - 1) * t->h + c.d) / (16 / esize) > (int64_t)INT32_MAX ||
         std::max(t->b, t->l) / (16 / esize) > (int64_t)UINT32_MAX)
       s.wide = false;
   int ctas, fixed, big = kFwdBig;

@@ -549,8 +549,9 @@ __device__ __forceinline__ float inv_std(float sum_sq, float inv_d, float eps) {
 
 // How a problem is laid over the GPU, with `ctas` CTAs of an SM resident where
 // two ring stages of each fit, else fewer. `wide` goes by room and reach too:
-// one stage has to fit, a token's vectors have to lie within 2^31 elements of
-// its first, and strides below 2^32 vectors.
+// one stage has to fit (all but the float32 backward of more than 7168 features
+// with dy, a sigmoid gate, b_post and a norm of y), a token's vectors have to
+// lie within 2^31 vectors of its first, and strides below 2^32 vectors.
 struct SubShape {
   int per, team, teams, threads, tok, groups, tokens, parts, stages, vecs, smem;
   bool wide;

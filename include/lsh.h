@@ -252,8 +252,13 @@ lsh_status lsh_rev_bwd(const lsh_problem* p, const lsh_ff_problem* f, const void
  * A problem names the strides of each group of activations; all three zero
  * means the contiguous [B, H, L, d]. Strides of dimensions longer than 1 are
  * positive and describe distinct elements (no expanded dimensions).
- * Activations need the alignment of their element type; when pointers and
- * strides are multiples of 16 bytes and d of 8, the wide-access kernels run.
+ * Activations need the alignment of their element type; when pointers (those of
+ * parameters too) and strides are multiples of 16 bytes and d of 8, the
+ * wide-access kernels run, else element-wise ones. The norms and the residual
+ * take the latter as well where a token's heads lie 2^31 or more such vectors
+ * apart or a stride is 2^32 of them or more, and in one backward pass whose
+ * rows leave them no room: float32, dy, a sigmoid gate, b_post and a norm of y,
+ * D above 7168.
  *
  * An output activation may be the same array (pointer and strides) as an
  * activation input of the same call, except that lsh_residual_bwd's dx may

@@ -102,3 +102,59 @@ def test_sigmoid_gate_over_its_range_in_float32():
     base._close(df, s * dy64, "f32", np.abs(s * dy64), 13)
     want = dy64 * f64 * s * t
     base._close(dz, want, "f32", np.abs(want), 23)
+
+
+def test_head_strides_within_reach_of_the_wide_kernels():
+    """Rows whose heads lie 2^31 elements apart, but 2^29 vectors of 16 bytes,
+    give bit for bit what near ones give: the same kernel runs."""
+    from efficient_transformer_lsh_b200 import _lib
+    torch = base._torch()
+    B, H, L, d = 1, 2, 300, 64
+    far = (1 << 31) + 64                          # 8.6 GB in float32
+    buf = torch.empty(far + L * d, dtype=torch.float32, device="cuda")
+    big = buf.as_strided((B, H, L, d), (far, far, d, 1))
+    x, f = torch.randn(2, B, H, L, d, device="cuda")
+    w, b = torch.randn(2, H * d, device="cuda")
+    big.copy_(x)
+    near, got, h1, h2 = (torch.empty_like(x) for _ in range(4))
+    strides = (far, far, d)
+    _lib.lsh_norm_fwd(_lib.make_norm_problem(B, H, L, d, "f32", 1, 1e-5), x, w, b, near)
+    _lib.lsh_norm_fwd(_lib.make_norm_problem(B, H, L, d, "f32", 1, 1e-5, x=strides), big, w, b, got)
+    assert torch.equal(near, got)
+    res = [B, H, L, d, "f32", 1, 0, 0, False, 1e-5, 1e-5, 0.5, 1.0, 0.1, 0]
+    _lib.lsh_residual_fwd(_lib.make_residual_problem(*res), f, x, None, w, b, None, None, 5, 0,
+                          None, h1, None)
+    _lib.lsh_residual_fwd(_lib.make_residual_problem(*res, f=strides), f, big, None, w, b, None,
+                          None, 5, 0, None, h2, None)
+    assert torch.equal(h1, h2)
+
+
+def test_head_strides_past_reach_of_the_wide_kernels():
+    """2^31 vectors of 16 bytes between two heads: the element-wise kernel,
+    with 64-bit offsets."""
+    from efficient_transformer_lsh_b200 import _lib
+    torch = base._torch()
+    B, H, L, d = 1, 2, 3, 64
+    far = (1 << 33) + 64                          # 34 GB
+    buf = torch.empty(far + L * d, dtype=torch.float32, device="cuda")
+    big = buf.as_strided((B, H, L, d), (far, far, d, 1))
+    x, x64 = base._put(np.random.default_rng(1).standard_normal((B, H, L, d)), "f32")
+    h = torch.empty_like(x)
+    n = _lib.make_norm_problem(B, H, L, d, "f32", 1, 1e-5, x=(far, far, d), h=(far, far, d))
+    big.copy_(x)
+    _lib.lsh_norm_fwd(n, big, None, None, big)    # in place
+    want = orc.norm_forward(x64, "layer", 1e-5)
+    base._close(big, want, "f32", base._norm_mag(x64, "layer", 1e-5, None, None))
+    n = _lib.make_norm_problem(B, H, L, d, "f32", 1, 1e-5, x=(far, far, d))
+    big.copy_(x)
+    _lib.lsh_norm_fwd(n, big, None, None, h)
+    base._close(h, want, "f32", base._norm_mag(x64, "layer", 1e-5, None, None))
+
+
+def test_rows_too_wide_for_the_wide_backward():
+    """float32, 8192 features, a sigmoid gate, both norms and b_post: a stage of
+    the ring and the parameters leave the wide kernel no room."""
+    base.test_residual((1, 128, 40, 64, "f32", "layer", "layer", "sigmoid", False, 0.1, 1.0, 1.0,
+                        "head", "head", 0))
+    base.test_residual((1, 112, 40, 64, "f32", "layer", "layer", "sigmoid", False, 0.1, 1.0, 1.0,
+                        "head", "head", 0))
