@@ -171,11 +171,12 @@ def _seed(v, name):
 
 class Norm(_Driver):
     """h = xhat w + b over each token's H d features (``kind`` "layer" or
-    "rms"). Buffers: h, dx (their layouts), dw, db float32 [H d], and the
-    backward's workspace."""
+    "rms"). Buffers: h, and unless ``forward_only`` dx (their layouts), dw, db
+    float32 [H d] and the backward's workspace."""
 
     def __init__(self, B, H, L, kind="layer", eps=1e-5, dtype="bf16", d=64,
-                 x_layout: Layout = "head", h_layout: Layout = "head", device="cuda"):
+                 x_layout: Layout = "head", h_layout: Layout = "head", device="cuda",
+                 forward_only=False):
         super().__init__(B, H, L, d, dtype, device)
         if kind not in ("layer", "rms"):
             _refuse("Norm", f"kind {kind!r}")
@@ -187,10 +188,12 @@ class Norm(_Driver):
         self._D = (self.H * self.d,)
         self.h = self._buffer(self.sh)
         self._h = self.h.data_ptr()   # of the driver's own buffer
-        self.dx = self._buffer(self.sx)
-        self.dw = torch.empty(self._D, dtype=torch.float32, device=self.device)
-        self.db = torch.empty_like(self.dw)
-        self.ws = self._workspace(self.ws_bytes)
+        self.dx = self.dw = self.db = self.ws = None
+        if not forward_only:
+            self.dx = self._buffer(self.sx)
+            self.dw = torch.empty(self._D, dtype=torch.float32, device=self.device)
+            self.db = torch.empty_like(self.dw)
+            self.ws = self._workspace(self.ws_bytes)
 
     def forward(self, x, w=None, b=None, out=None, stream=None):
         if self._away():
@@ -207,6 +210,8 @@ class Norm(_Driver):
         """(dx, dw, db): gradients of sum(h * dh), with ``dres`` (the gradient
         that reaches x past the norm) added to dx. dw and db are formed where w
         and b are given, else None."""
+        if self.ws is None:
+            _refuse("Norm", "made forward_only")
         if self._away():
             return self._there(self.backward, x, dh, w, b, dres, out, stream)
         dx = self.dx if out is None else out
@@ -565,7 +570,7 @@ class ReversibleLayer(_Driver):
         self.ff_ws_bytes = self._sized(_lib.lsh_ff_workspace_size(self.f))
         self.ff_ws = self._workspace(self.ff_ws_bytes)
         self.norm1 = Norm(B, H, L, norm, eps, **kw)
-        self.norm2 = Norm(B, H, L, norm, eps, **kw)
+        self.norm2 = Norm(B, H, L, norm, eps, forward_only=True, **kw)
         join = dict(post=post, gate="vector" if gate else None, p=p, alpha=alpha, eps=eps,
                     slice0=slice0, **kw)
         self.join1 = Residual(B, H, L, norm=norm, **join)
@@ -576,7 +581,9 @@ class ReversibleLayer(_Driver):
         self.D, self.d_ff = 64 * self.H, int(d_ff)
         f32 = dict(dtype=torch.float32, device=self.device)
         act = lambda: self._buffer(self._strides("head"))
-        self.g, self.dm, self.dn, self.dx2 = act(), act(), act(), act()
+        self.g, self.dm = act(), act()
+        self.dn = self.rope.dx if rot else act()
+        self.dx2 = self.norm1.dx
         self.dW1 = torch.empty((self.D, self.d_ff), **f32)
         self.db1 = torch.empty((self.d_ff,), **f32)
         self.dW2 = torch.empty((self.d_ff, self.D), **f32)
@@ -679,12 +686,12 @@ class ReversibleLayer(_Driver):
                                            b=w.get("norm2_b"), offset=o1, **rng)
         dqk, dv = self.attn.backward(q, n, df, None, stream)
         if self.rope is not None:
-            dn = self.rope.backward_sum(dqk, dv, pos0=pos0, out=self.dn, stream=stream)
+            dn = self.rope.backward_sum(dqk, dv, pos0=pos0, stream=stream)
         else:
             dn = self.dn
             _lib.lsh_rope_bwd_sum(self._sum, dqk, dv, None, None, 0, dn, stream)
         _, dw, db = self.norm1.backward(x2, dn, w["norm1_w"], w.get("norm1_b"), dres=dx2,
-                                        out=self.dx2, stream=stream)
+                                        stream=stream)
         grads = dict(W1=self.dW1, b1=self.db1, W2=self.dW2, b2=self.db2, norm1_w=dw, norm1_b=db,
                      gate1=d1[0], post1_w=d1[1], post1_b=d1[2], norm2_w=d1[3], norm2_b=d1[4],
                      gate2=d2[0], post2_w=d2[1], post2_b=d2[2])

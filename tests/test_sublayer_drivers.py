@@ -133,3 +133,28 @@ def test_rope_tables_hold_64_bits(sl):
     for base in (0.0, -2.0, float("inf")):
         with pytest.raises(_lib.LshError):
             sl.rope_frequencies(64, base)
+
+
+@pytest.mark.parametrize("rot", [0, 64])
+def test_the_layer_holds_no_buffer_that_nothing_writes(sl, rot):
+    """Its second norm runs forward only; the gradients of the first norm and of
+    the rotary positions are the drivers' own buffers."""
+    import torch
+    lay = sl.ReversibleLayer(1, 2, 128, 2, 1, 64, True, 256, 128, rot=rot, **CPU)
+    assert lay.dx2 is lay.norm1.dx
+    if rot:
+        assert lay.dn is lay.rope.dx
+    assert [getattr(lay.norm2, k) for k in ("dx", "dw", "db", "ws")] == [None] * 4
+    size = lay.dx2.numel()
+    held = {}
+    for o in (lay, lay.norm1, lay.norm2, lay.join1, lay.join2, *([lay.rope] if rot else [])):
+        for k, v in vars(o).items():
+            if isinstance(v, torch.Tensor) and v.numel() == size and v.dtype == torch.bfloat16:
+                held[v.data_ptr()] = k
+    # n, m twice, q and its gradient; y, x, dx and df of each join; g, dm, and dn
+    # without rotary positions, dx2
+    assert len(held) == 3 + (2 if rot else 1) + 8 + 2 + 1
+    n = sl.Norm(1, 2, 3, forward_only=True, **CPU)
+    x = torch.zeros(1, 2, 3, 64, dtype=torch.bfloat16)
+    with pytest.raises(_lib.LshError):
+        n.backward(x, x)
