@@ -158,3 +158,124 @@ def test_rows_too_wide_for_the_wide_backward():
                         "head", "head", 0))
     base.test_residual((1, 112, 40, 64, "f32", "layer", "layer", "sigmoid", False, 0.1, 1.0, 1.0,
                         "head", "head", 0))
+
+
+ALIAS_SHAPES = [(8, 64, 12000), (40, 64, 2600), (3, 7, 7000), (5, 64, 9001)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,d,L", ALIAS_SHAPES)
+def test_norm_outputs_over_inputs(H, d, L, dtype):
+    """Every array that an output may share gives the bits of separate ones, over
+    several rounds of tokens."""
+    from efficient_transformer_lsh_b200 import _lib
+    torch = base._torch()
+    td = torch.bfloat16 if dtype == "bf16" else torch.float32
+    D, B = H * d, 1
+    src = {k: torch.randn(B, H, L, d, device="cuda").to(td) for k in ("x", "dh", "dres")}
+    w, b = torch.randn(2, D, device="cuda")
+    n = _lib.make_norm_problem(B, H, L, d, dtype, _lib.LSH_NORM_LAYER, 1e-5)
+    size = _lib.lsh_norm_bwd_workspace_size(n)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+
+    def run(fwd, back):
+        t = {k: v.clone() for k, v in src.items()}
+        h = t[fwd] if fwd else torch.empty_like(t["x"])
+        _lib.lsh_norm_fwd(n, t["x"], w, b, h)
+        h = h.clone()
+        t = {k: v.clone() for k, v in src.items()}
+        dx = t[back] if back else torch.empty_like(t["x"])
+        dw, db = torch.empty(2, D, device="cuda")
+        _lib.lsh_norm_bwd(n, t["x"], w, t["dh"], t["dres"], dx, dw, db, ws, size)
+        return h, dx, dw, db
+
+    want = run(None, None)
+    for fwd, back in (("x", "x"), (None, "dh"), (None, "dres")):
+        assert all(torch.equal(p, q) for p, q in zip(run(fwd, back), want)), (fwd, back)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("gate", [None, "vector", "sigmoid"])
+@pytest.mark.parametrize("H,d,L", ALIAS_SHAPES)
+def test_residual_outputs_over_inputs(H, d, L, gate, dtype):
+    from efficient_transformer_lsh_b200 import _lib
+    torch = base._torch()
+    td = torch.bfloat16 if dtype == "bf16" else torch.float32
+    D, B, sig = H * d, 1, gate == "sigmoid"
+    names = ["x", "f", "y", "dy", "dh"] + (["z"] if sig else [])
+    src = {k: torch.randn(B, H, L, d, device="cuda").to(td) for k in names}
+    w_post, b_post, w, b, vec = torch.randn(5, D, device="cuda")
+    kind = {None: _lib.LSH_GATE_NONE, "vector": _lib.LSH_GATE_VECTOR,
+            "sigmoid": _lib.LSH_GATE_SIGMOID}[gate]
+    post = _lib.LSH_NORM_LAYER if gate else _lib.LSH_NORM_NONE
+    q = _lib.make_residual_problem(B, H, L, d, dtype, post, _lib.LSH_NORM_LAYER, kind, False, 1e-5,
+                                   1e-5, 0.5, 1.5, 0.1)
+    size = _lib.lsh_residual_bwd_workspace_size(q)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    wp, bp = (w_post, b_post) if gate else (None, None)
+
+    def arrays(shared):
+        """Copies of the inputs, and each output's array: an input's or its own."""
+        t = {k: v.clone() for k, v in src.items()}
+        return t, lambda o: t[shared[o]] if o in shared else torch.empty_like(t["x"])
+
+    def forward(**shared):
+        t, out = arrays(shared)
+        y, h = out("y"), out("h")
+        g = t["z"] if sig else vec if gate else None
+        _lib.lsh_residual_fwd(q, t["x"], t["f"], g, wp, bp, w, b, 7, 0, None, y, h)
+        return y, h
+
+    def backward(**shared):
+        t, out = arrays(shared)
+        dx, df, dz = out("dx"), out("df"), out("dz") if sig else None
+        g, dg = (t["z"], dz) if sig else (vec, torch.empty_like(vec)) if gate else (None, None)
+        grads = [torch.empty_like(w) if k else None for k in (gate, gate, True, True)]
+        _lib.lsh_residual_bwd(q, t["dy"], t["dh"], t["y"], t["f"], g, wp, bp, w, 7, 0, None, dx, df,
+                              dg, *grads, ws, size)
+        return [v for v in (dx, df, dg, *grads) if v is not None]
+
+    branch = ["f"] + (["z"] if sig else [])
+    want = [v.clone() for v in forward()]
+    for shared in [dict([(o, i)]) for o in ("y", "h") for i in ["x"] + branch] + \
+            [dict(y="x", h="f"), dict(y="f", h="x")]:
+        assert all(torch.equal(p, r) for p, r in zip(forward(**shared), want)), shared
+    want = [v.clone() for v in backward()]
+    every = ["y", "dy", "dh"]
+    cases = [dict(dx=i) for i in every] + [dict(df=i) for i in every + branch]
+    cases += [dict(dx="dy", df="f"), dict(dx="dh", df="dy"), dict(dx="y", df="dh")]
+    if sig:
+        cases += [dict(dz=i) for i in every + branch]
+        cases += [dict(dx="dy", df="f", dz="z"), dict(dx="dh", df="z", dz="f")]
+    for shared in cases:
+        assert all(torch.equal(p, r) for p, r in zip(backward(**shared), want)), shared
+
+
+@pytest.mark.parametrize("H,d,dtype", [(3, 64, "bf16"), (40, 64, "bf16"), (3, 64, "f32"),
+                                       (3, 10, "f32"), (2, 512, "f32")])
+def test_elementwise_outputs_over_inputs(H, d, dtype):
+    from efficient_transformer_lsh_b200 import _lib
+    torch = base._torch()
+    td = torch.bfloat16 if dtype == "bf16" else torch.float32
+    B, L = 2, 901
+    x = torch.randn(B, H, L, d, device="cuda").to(td)
+    q = _lib.make_dropout_problem(B, H, L, d, dtype, 0.3)
+    want, same = torch.empty_like(x), x.clone()
+    _lib.lsh_dropout_fwd(q, x, 3, 0, None, want)
+    _lib.lsh_dropout_fwd(q, same, 3, 0, None, same)
+    assert torch.equal(same, want)
+    turns = torch.randint(-(1 << 62), 1 << 62, (d // 2,), device="cuda")
+    for inter in (False, True):
+        p = _lib.make_rope_problem(B, H, L, d, dtype, d - d // 4 * 2, inter, False, 1.0)
+        for fn in (_lib.lsh_rope_fwd, _lib.lsh_rope_bwd):
+            same = x.clone()
+            fn(p, x, turns, None, 9, want)
+            fn(p, same, turns, None, 9, same)
+            assert torch.equal(same, want)
+        if dtype == "f32":
+            dv = torch.randn_like(x)
+            _lib.lsh_rope_bwd_sum(p, x, dv, turns, None, 9, want)
+            for over in (0, 1):
+                t = [x.clone(), dv.clone()]
+                _lib.lsh_rope_bwd_sum(p, *t, turns, None, 9, t[over])
+                assert torch.equal(t[over], want)
