@@ -279,3 +279,118 @@ def test_elementwise_outputs_over_inputs(H, d, dtype):
                 t = [x.clone(), dv.clone()]
                 _lib.lsh_rope_bwd_sum(p, *t, turns, None, 9, t[over])
                 assert torch.equal(t[over], want)
+
+
+@pytest.mark.parametrize("H,d,dtype", [(3, 64, "bf16"), (2, 64, "f32"), (3, 7, "bf16")])
+def test_residual_of_a_later_slice(H, d, dtype):
+    """slice0: the mask of the rows that the shard holds of the whole problem."""
+    from efficient_transformer_lsh_b200 import sublayer as sl
+    torch = base._torch()
+    B, L, slice0, seed = 2, 33, 1001, 17
+    shape = (B, H, L, d)
+    g = np.random.default_rng(d)
+    (x, x_), (f, f_), (dy, dy_) = (base._put(g.standard_normal(shape), dtype) for _ in range(3))
+    r = sl.Residual(B, H, L, p=0.3, dtype=dtype, d=d, slice0=slice0)
+    fac = orc.dropout_factor(shape, 0.3, seed, 5, slice0=slice0)
+    y, _ = r.forward(x, f, seed=seed, offset=5)
+    mag = np.abs(x_) + fac * np.abs(f_)
+    base._close(y, x_ + fac * f_, dtype, mag, 4)       # scale, product, sum
+    base._close(r.backward(dy, f, seed=seed, offset=5)[1], fac * dy_, dtype, fac * np.abs(dy_), 4)
+    # the mask is that of the dropout alone, and of the whole problem's rows
+    keep = sl.Dropout(B, H, L, 0.3, dtype, d, slice0=slice0).forward(torch.ones_like(x), seed, 5) != 0
+    assert torch.equal(keep, torch.from_numpy(fac > 0).cuda())
+    n = -(-(slice0 + B * H) // H)
+    whole = orc.dropout_factor((n, H, L, d), 0.3, seed, 5).reshape(n * H, L, d)
+    assert np.array_equal(whole[slice0:slice0 + B * H].reshape(shape), fac)
+
+
+@pytest.mark.parametrize("H,d,dtype", [(8, 64, "bf16"), (40, 64, "f32"), (3, 7, "f32")])
+def test_two_epsilons_and_no_dx(H, d, dtype):
+    """eps_post is f's, eps is y's; dx may be NULL, and changes nothing else."""
+    from efficient_transformer_lsh_b200 import _lib
+    torch = base._torch()
+    B, L, D = 2, 19, H * d
+    shape, ep, en = (B, H, L, d), 0.5, 2.0
+    g = np.random.default_rng(H)
+    (x, x_), (f, f_), (y, y_), (dy, dy_), (dh, dh_) = (base._put(g.standard_normal(shape), dtype)
+                                                       for _ in range(5))
+    q = _lib.make_residual_problem(B, H, L, d, dtype, _lib.LSH_NORM_LAYER, _lib.LSH_NORM_RMS,
+                                   _lib.LSH_GATE_NONE, False, ep, en, 1.0, 1.0, 0.0)
+    out, h = torch.empty_like(x), torch.empty_like(x)
+    _lib.lsh_residual_fwd(q, x, f, None, None, None, None, None, 0, 0, None, out, h)
+    fm = base._norm_mag(f_, "layer", ep, None, None)
+    base._close(out, x_ + orc.norm_forward(f_, "layer", ep), dtype, np.abs(x_) + fm)
+    o = out.double().cpu().numpy()
+    base._close(h, orc.norm_forward(o, "rms", en), dtype, base._norm_mag(o, "rms", en, None, None))
+    size = _lib.lsh_residual_bwd_workspace_size(q)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    got = []
+    for dx in (torch.empty_like(x), None):
+        df = torch.empty_like(x)
+        grads = [torch.empty(D, device="cuda") for _ in range(4)]
+        _lib.lsh_residual_bwd(q, dy, dh, y, f, None, None, None, None, 0, 0, None, dx, df, None,
+                              *grads, ws, size)
+        got.append([df, *grads])
+        if dx is not None:
+            t, dw, db = orc.norm_backward(y_, "rms", en, None, dh_, dy_)
+            m, ym = base._norm_back_mag(y_, "rms", en, None, dh_)
+            tm = m + np.abs(dy_)
+            base._close(dx, t, dtype, tm)
+            want, wp, bp = orc.norm_backward(f_, "layer", ep, None, t)
+            m, fm = base._norm_back_mag(f_, "layer", ep, None, tm)
+            n = 2 * base.K
+            base._close(df, want, dtype, m, n)
+            flat = lambda a: a.sum((0, 2)).reshape(D)
+            for a, b, c in zip(grads, (wp, bp, dw, db), (flat(tm * fm), flat(tm),
+                                                         flat(np.abs(dh_) * ym), flat(np.abs(dh_)))):
+                base._close(a, b, "f32", c, B * L + n)
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def test_rotary_with_given_frequencies_and_multiplier():
+    from efficient_transformer_lsh_b200 import sublayer as sl
+    B, H, L, d, rot = 2, 3, 40, 64, 24
+    g = np.random.default_rng(8)
+    shape = (B, H, L, d)
+    (x, x_), (dy, dy_) = (base._put(g.standard_normal(shape), "f32") for _ in range(2))
+    freqs = list(g.uniform(-3.0, 3.0, rot // 2))
+    r = sl.Rotary(B, H, L, rot, True, frequencies=freqs, amp=1.75, dtype="f32")
+    pos = 5 + np.arange(L)
+    mag = lambda a: 1.75 * base._pair_sum(np.abs(a), rot, True)
+    base._close(r.forward(x, pos0=5), orc.rope(x_, freqs, pos, rot, True, 1.75), "f32", mag(x_), 9)
+    base._close(r.backward(dy, pos0=5), orc.rope(dy_, freqs, pos, rot, True, 1.75, True), "f32",
+                mag(dy_), 9)
+    # without a multiplier it is 1, whatever a scaling's would be
+    one = sl.Rotary(B, H, L, rot, True, frequencies=freqs, dtype="f32")
+    assert one.amp == 1.0
+    base._close(one.forward(x), orc.rope(x_, freqs, np.arange(L), rot, True), "f32", mag(x_), 9)
+
+
+def test_reversible_layer_of_more_heads_with_scaled_adjacent_pairs():
+    """The whole layer against the oracle at 4 heads, 1024 tokens, half of each
+    head turned in adjacent pairs with a scaled table; tolerances as in the
+    stage by stage test (its last lines)."""
+    from efficient_transformer_lsh_b200 import _lib
+    from efficient_transformer_lsh_b200 import sublayer as sl
+    B, H, L, dff, rot, scaling = 1, 4, 1024, 512, 32, ("yarn", 4.0, 256)
+    post, gate, norm, p, seed = "rms", True, "layer", 0.1, 21
+    _, w, w64, acts, R = base._layer(post, gate, norm, rot, p, True, 9, B, H, L, dff)
+    run = sl.ReversibleLayer(B, H, L, 16, 2, 64, True, dff, 256, norm=norm, post=post, gate=gate,
+                             p=p, alpha=0.5, rot=rot, interleaved=True, scaling=scaling)
+    (x1, x1_), (x2, x2_), (dy1, dy1_), (dy2, dy2_) = acts
+    y1, y2 = run.forward(x1, x2, R, w, seed=seed, pos0=100)
+    num = lambda t: t.double().cpu().numpy()
+    y1_, y2_ = num(y1), num(y2)
+    rx1, rx2, dx1, dx2, grads = run.backward(y1, y2, dy1, dy2, w, seed=seed, pos0=100)
+    assert _lib.lsh_device_status() == 0
+    freqs, amp = sl.rope_frequencies(rot, scaling=scaling)
+    fac = [orc.dropout_factor(run.shape, p, seed, o) for o in (0, 1 << 63)]
+    c = dict(norm=norm, post=post, gate=gate, alpha=0.5, eps=1e-5, freqs=freqs, rot=rot,
+             interleaved=True, amp=amp, pos=100 + np.arange(L), chunk=64, causal=True, scale=0.125,
+             fac1=fac[0], fac2=fac[1])
+    perm = run.attn.perm.cpu().numpy().astype(np.int64)
+    wx1, wx2, wdx1, wdx2, wg = orc.layer_backward(y1_, y2_, dy1_, dy2_, perm, w64, c)
+    for got, want in ((rx1, x1_), (rx2, x2_), (rx1, wx1), (rx2, wx2), (dx1, wdx1), (dx2, wdx2),
+                      *((grads[k], wg[k]) for k in w)):
+        a = num(got)
+        assert np.linalg.norm(a - want) <= 0.1 * np.linalg.norm(want)
