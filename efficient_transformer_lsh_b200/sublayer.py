@@ -419,7 +419,9 @@ def _frequencies(rot, base, scaling):
         s = D(float(scaling[1])) if kind else D(1)
         if kind == "ntk":
             b *= s ** (D(rot) / (rot - 2))
-        f = [b ** (D(-2 * i) / rot) for i in range(rot // 2)]
+        step, f = b ** (D(-2) / rot), [D(1)]   # one power: each takes 30 us
+        while len(f) < rot // 2:
+            f.append(f[-1] * step)
         if kind == "linear":
             f = [v / s for v in f]
         elif kind == "yarn":
