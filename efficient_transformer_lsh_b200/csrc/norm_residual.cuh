@@ -19,8 +19,10 @@
 // The bound is HBM where the copies of coming tokens are in flight while a
 // token is computed: each thread copies its own features of each input of the
 // next tokens to a ring in shared memory (cp.async, 16 bytes a copy) and reads
-// them back itself, so the ring needs no barrier. After that it is the number
-// of instructions: arithmetic runs on pairs (fma.rn.f32x2 and its like), and
+// them back itself, so the ring needs no barrier. Beyond that it is latency: a
+// token's dependent steps (statistics, shuffles, shared memory) at the few warps
+// that the registers leave, with issue slots about half used. Fewer steps help:
+// arithmetic runs on pairs (fma.rn.f32x2 and its like), and
 // teams are as small as registers allow (16 threads for 512 features), so that
 // addresses, shuffles and statistics, which cost the same for any team of at
 // most a warp, serve several tokens at once.

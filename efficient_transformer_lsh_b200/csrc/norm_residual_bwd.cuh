@@ -18,9 +18,10 @@
 //
 // 64K tokens of 512 features in bf16: a norm's 49.8 us with the sum of the
 // partials (268 MB, 5.4 TB/s); with everything on 93.8 us (403 MB, 4.3 TB/s),
-// bound by its instructions (about 765 a token and warp, of which 130 are the
-// dropout's) at the two warps a scheduler that 230 registers leave (three of
-// 168 registers spill: 102.7 us where this was 100.3). float32: a norm
+// bound by latency at the two warps a scheduler that 230 registers leave: its
+// 765 warp instructions a token (130 of them the dropout's) issue in 43 us, half
+// of the slots, and its bytes take 61 (three warps of 168 registers spill: 102.7
+// us where this was 100.3). float32: a norm
 // of 64K tokens 93 us, 5.8 TB/s (HBM).
 #pragma once
 

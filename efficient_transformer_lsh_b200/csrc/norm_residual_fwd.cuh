@@ -10,10 +10,12 @@ namespace {
 // One pass: the row of f (or x) in registers, its statistics, the gate, the
 // dropout, the add, y's statistics and h, each activation read and written
 // once. 64K tokens of 512 features: a norm alone 25.9 us (134 MB, 5.2 TB/s),
-// with everything on 52.9 us (268 MB, 5.1 TB/s); there the instructions of a
-// token (about 520 a warp) take as long as its bytes: bf16 unpacking, the two
-// statistics, ten Philox rounds for every 8 features. 4 x 8192 tokens of 4096
-// features, a norm: 82 us (537 MB, 6.5 TB/s: HBM).
+// with everything on 52.9 us (268 MB, 5.1 TB/s); there a token's 520 warp
+// instructions (bf16 unpacking, the two statistics, ten Philox rounds for every
+// 8 features) issue in 29 us, its bytes take 41, and 16 warps an SM overlap them
+// in part. 4 x 8192 tokens of 4096 features, a norm: 82 us (537 MB, 6.5 TB/s:
+// HBM); 8192 of them with everything on 71 us (floor 41: two barriers a
+// LayerNorm, one CTA an SM).
 //
 // Parameters, in order: W, P1 = gate w_post (a sigmoid gate is not in it), then
 // B, P0 = gate b_post where there is one of them: the products are formed once
